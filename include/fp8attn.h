@@ -75,7 +75,8 @@ typedef enum {
   FP8ATTN_ERR_TIMEOUT = 3,     /* a device-side wait gave up (work skipped) */
   FP8ATTN_ERR_UNSUPPORTED = 4, /* valid but unsupported (head_dim != 128, ...) */
   FP8ATTN_ERR_NONFINITE = 5,   /* an observed amax was infinite (not pushed) */
-  FP8ATTN_ERR_SEQLENS = 6      /* cu_seqlens inconsistent with batch/max_seqlen */
+  FP8ATTN_ERR_SEQLENS = 6,     /* cu_seqlens inconsistent with batch/max_seqlen */
+  FP8ATTN_ERR_PAGES = 7        /* paged cache: a page or slot outside it, or too few free pages */
 } fp8attn_status;
 
 /* Per-layer quantisation mode (host-side selection). */
@@ -495,6 +496,147 @@ int fp8attn_quantize_qkv_noalloc(const void* q, const void* k, const void* v, in
  * point for the current device (synchronises `stream`); after a TIMEOUT the
  * barrier words are reset too.  Returns an fp8attn_status. */
 int fp8attn_quantize_qkv_noalloc_error(void* stream);
+
+/* ------------------------------------------------------------------ */
+/* Paged KV cache                                                      */
+/*                                                                     */
+/* K and V kept from step to step ("Quantized KV Cache", vLLM-Omni     */
+/* docs: the KV cache quantised to FP8 with per-tensor scales, listed  */
+/* layers in the native dtype; the pages say nothing of its layout).   */
+/* A cache holds num_pages pages of page_size slots (a power of two,   */
+/* 8 to 1024); element (slot s, head h, channel d) of K or V is at     */
+/*   base + (s / page_size) * page_stride + (s % page_size) *          */
+/*   slot_stride + h * head_stride + d                                 */
+/* in elements: E4M3 codes (1 byte) or bf16.  K and V share the        */
+/* strides; bases and strides are multiples of 16 bytes.  Token-major  */
+/* [pages, page_size, heads, 128] and head-major [pages, heads,        */
+/* page_size, 128] caches, and K and V interleaved in one allocation,  */
+/* differ in strides alone.  A block table row lists a request's pages */
+/* in order.  d_error arguments: optional device int32 that receives   */
+/* error bits, as in fp8attn_varlen_fwd.                               */
+/* ------------------------------------------------------------------ */
+
+/* Device pointers to a layer's static {qs_q, qs_k, qs_v} and {ds_q, ds_k,
+ * ds_v}: a cache outlives the layer's current scales, so its scales are the
+ * static ones.  NULL on a bad argument or without static bounds. */
+const float* fp8attn_static_quant_scale_ptr(fp8attn_ctx* ctx, int layer);
+const float* fp8attn_static_descale_ptr(fp8attn_ctx* ctx, int layer);
+
+/* Block tables and the slot map of one step, from the requests' lengths.
+ * Row b holds d_seq_lens[b] tokens after this step, the last d_new_lens[b] of
+ * which are written in it.  It needs ceil(seq / page_size) pages and holds
+ * d_owned[b]: the first entries of its block table row ([rows, table_width],
+ * row stride table_stride).  A row that holds more gives its last pages back
+ * (a request that ended has length 0), a row that holds fewer gets new ones,
+ * in row order: first the pages given back in this call, then d_free_pages
+ * (int32[num_pages], the first d_pool[0] of them free) from its end.  What is
+ * given back and not taken goes to the free list's end, reversed, so taking
+ * pages and giving the same ones back restores the list.  d_pool: int32[2],
+ * {free pages, 0}; the second word is the kernel's and is 0 between calls.
+ *   d_cu_new: int32[rows + 1], first new token of each row;
+ *   d_slots: int64[max_tokens], d_positions: int32[max_tokens] (16-byte
+ *     aligned): slot and position of each new token; behind the last, up to
+ *     max_tokens, slots are -1 and positions 0 (a step captured at a fixed
+ *     size: fp8attn_kv_write skips them).
+ * Block table entries that no new page takes stay as they are.  Rows must not
+ * share pages that this call gives back; calls on one pool must not overlap.
+ * Device-side errors change nothing of the tables and the pool and give an
+ * empty step (cu all 0, slots -1): SEQLENS (new < 0, new > seq, seq beyond
+ * table_width pages, owned outside [0, table_width], more than max_tokens new
+ * tokens), PAGES (too few free pages, d_pool[0] out of range).  A page id
+ * outside [0, num_pages) in a table or the free list sets PAGES too; its
+ * tokens get slot -1.  Errors: INVALID (null or misaligned pointers, rows < 0,
+ * num_pages < 1, table_width < 1, max_tokens < 0), UNSUPPORTED (page_size,
+ * rows > 16384, num_pages >= 2^30, max_tokens >= 2^31), CUDA.  rows == 0
+ * launches nothing, and needs max_tokens == 0. */
+fp8attn_status fp8attn_kv_assign_pages(const int32_t* d_seq_lens, const int32_t* d_new_lens,
+                                       int rows, int page_size, int32_t* d_block_tables,
+                                       int64_t table_stride, int table_width, int32_t* d_owned,
+                                       int32_t* d_free_pages, int num_pages, int32_t* d_pool,
+                                       int64_t max_tokens, int32_t* d_cu_new, int64_t* d_slots,
+                                       int32_t* d_positions, int32_t* d_error, void* stream);
+
+/* Write the K and V of new tokens into their slots.  k, v: bf16 sources as in
+ * fp8attn_quantize_qkv, one row per entry of d_slots (int64[tokens]).
+ * d_quant_scale_qkv: device {qs_q, qs_k, qs_v}; the cache then holds E4M3
+ * codes e4m3(fl32(x * qs)), as the quantisation kernels cast.  NULL: a bf16
+ * cache, x unchanged.  A negative slot is skipped; one beyond the cache is
+ * skipped and sets PAGES.  Slots must be distinct: of two tokens with one
+ * slot either's 16-byte pieces may remain.  Errors: INVALID, UNSUPPORTED
+ * (head_dim != 128, page_size, strides or alignment, tokens * heads >= 2^31),
+ * CUDA.  tokens == 0 launches nothing. */
+fp8attn_status fp8attn_kv_write(const void* k, const void* v, int64_t tok_stride,
+                                int64_t head_stride, const int64_t* d_slots, int64_t tokens,
+                                int num_kv_heads, int head_dim, void* k_cache, void* v_cache,
+                                int64_t page_stride, int64_t slot_stride,
+                                int64_t cache_head_stride, int num_pages, int page_size,
+                                const float* d_quant_scale_qkv, int32_t* d_error, void* stream);
+
+/* Bytes of device workspace fp8attn_kv_tree_fwd needs for these bounds (0 if
+ * it needs none, or on a bad argument). */
+size_t fp8attn_kv_tree_workspace_bytes(int rows, int max_q_len, int max_seqlen, int num_heads,
+                                       int num_kv_heads);
+
+/* Attention of new tokens over the cache: a drafted tree, a chain, or a single
+ * token per request.  Request b's n_b = cu_q[b+1] - cu_q[b] queries (rows
+ * cu_q[b].. of q, bf16 [total_q, num_heads, 128] with element strides, 16-byte
+ * aligned) are the last n_b of its d_seq_lens[b] positions, whose K and V are
+ * in the cache already.  Query i sees every position before those, and node m
+ * of them if bit m % 64 of d_tree_mask[i][m / 64] is set (int64 [total_q,
+ * mask_words], rows cu_q[b] + i); without a mask, m <= i.  Query head h reads
+ * KV head h / (num_heads / num_kv_heads).  A query that sees nothing gives 0;
+ * K and V that a query does not see do not touch it, Inf and NaN included.
+ *   out[i] = ds_v sum_j p_j v_j / sum_j p_j,
+ *   p_j = exp(softmax_scale ds_k q_i . k_j - max)
+ * d_descale_qkv: device {ds_q, ds_k, ds_v} for an E4M3 cache (q is bf16, ds_q
+ * unused); NULL for a bf16 cache.  softmax_scale 0 selects 1/sqrt(head_dim).
+ * max_q_len, max_seqlen: bounds of n_b and of the lengths.  out: bf16 packed
+ * [total_q, num_heads, 128]; rows of no request stay as they are.  workspace:
+ * fp8attn_kv_tree_workspace_bytes of device memory (16-byte aligned), used by
+ * this call alone while it runs; calls that overlap need their own.  Results
+ * do not depend on timing: the same call gives the same bits.
+ * Device-side: SEQLENS (a request with n_b outside [0, max_q_len], length
+ * below n_b, above max_seqlen or beyond table_width pages, queries beyond
+ * total_q, or more than 64 mask_words nodes: it is left out, its rows stay as
+ * they are), PAGES (a page id outside the cache: its keys and values are read
+ * as zeros), TIMEOUT.
+ * Errors: INVALID (null pointers, negative sizes, num_heads not a multiple of
+ * num_kv_heads, a workspace too small, a bad softmax_scale), UNSUPPORTED
+ * (head_dim != 128, page_size, strides or alignment, rows > 2048, total_q *
+ * num_heads >= 2^31, bounds that allow 2^31 or more 128-key tiles), CUDA.
+ * rows == 0 or total_q == 0 launches nothing. */
+fp8attn_status fp8attn_kv_tree_fwd(const void* q, int64_t q_tok_stride, int64_t q_head_stride,
+                                   const void* k_cache, const void* v_cache,
+                                   int64_t page_stride, int64_t slot_stride,
+                                   int64_t cache_head_stride, int num_pages, int page_size,
+                                   const int32_t* d_block_tables, int64_t table_stride,
+                                   int table_width, const int32_t* d_seq_lens,
+                                   const int32_t* d_cu_q, int rows, int max_q_len,
+                                   int max_seqlen, int64_t total_q, int num_heads,
+                                   int num_kv_heads, int head_dim, const float* d_descale_qkv,
+                                   const int64_t* d_tree_mask, int mask_words,
+                                   float softmax_scale, void* out, void* workspace,
+                                   size_t workspace_bytes, int32_t* d_error, void* stream);
+
+/* After verification: request b keeps d_keep_lens[b] of its n_b drafted
+ * nodes, d_paths[b][0] < d_paths[b][1] < ... (int32 [rows, depth], row stride
+ * path_stride); their K and V rows move, in place, to nodes 0, 1, ... of the
+ * last n_b = cu_q[b+1] - cu_q[b] of its d_seq_lens[b] positions.  The caller
+ * then shortens the request to seq - n_b + keep tokens.  elem_bytes: 1 (E4M3)
+ * or 2 (bf16).  Requests must not share the pages their nodes lie in.
+ * Device-side: SEQLENS (keep outside [0, min(depth, n_b)], a path that does
+ * not rise or leaves [0, n_b), bad lengths: the request is left out), PAGES
+ * (a page id outside the cache: that node does not move).
+ * Errors: INVALID, UNSUPPORTED (head_dim != 128, page_size, strides or
+ * alignment), CUDA.  rows == 0 or depth == 0 launches nothing. */
+fp8attn_status fp8attn_kv_keep_path(void* k_cache, void* v_cache, int64_t page_stride,
+                                    int64_t slot_stride, int64_t cache_head_stride, int num_pages,
+                                    int page_size, int elem_bytes, int num_kv_heads, int head_dim,
+                                    const int32_t* d_block_tables, int64_t table_stride,
+                                    int table_width, const int32_t* d_seq_lens,
+                                    const int32_t* d_cu_q, int rows, const int32_t* d_paths,
+                                    int64_t path_stride, int depth, const int32_t* d_keep_lens,
+                                    int32_t* d_error, void* stream);
 
 /* Number of kernels the library has launched in this process (a counter
  * incremented on every successful launch; for accounting in benchmarks). */

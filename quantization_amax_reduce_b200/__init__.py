@@ -29,6 +29,7 @@ __all__ = [
     "launch_count", "load_scale_file", "save_scale_file", "apply_margin", "read_error_word",
     "quantize_qkv_noalloc", "quantize_qkv_noalloc_error", "RING",
     "head_sharded_dynamic_quantize", "regroup_heads", "TorchComm", "ulysses_attention",
+    "kv_assign_pages", "kv_write", "kv_tree_fwd", "kv_keep_path",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -45,6 +46,7 @@ HEAD_DIM = 128
 _STATUS = {
     0: "ok", 1: "invalid argument", 2: "CUDA error", 3: "device wait timed out",
     4: "unsupported configuration", 5: "non-finite amax", 6: "inconsistent cu_seqlens",
+    7: "page outside the cache, or too few free pages",
 }
 
 
@@ -109,6 +111,16 @@ def lib() -> ctypes.CDLL:
         "fp8attn_selftest_bounded_waits": (I, [ctypes.c_uint64, ctypes.POINTER(I), P]),
         "fp8attn_regroup_heads": (I, [P, P, I64, I, I, I, I, P]),
         "fp8attn_selftest_qk_scores": (I, [P, P, I64, P, P, P]),
+        "fp8attn_static_quant_scale_ptr": (P, [P, I]),
+        "fp8attn_static_descale_ptr": (P, [P, I]),
+        "fp8attn_kv_assign_pages": (I, [P, P, I, I, P, I64, I, P, P, I, P, I64, P, P, P, P, P]),
+        "fp8attn_kv_write": (I, [P, P, I64, I64, P, I64, I, I, P, P, I64, I64, I64, I, I, P, P,
+                                 P]),
+        "fp8attn_kv_tree_workspace_bytes": (ctypes.c_size_t, [I, I, I, I, I]),
+        "fp8attn_kv_tree_fwd": (I, [P, I64, I64, P, P, I64, I64, I64, I, I, P, I64, I, P, P, I, I,
+                                    I, I64, I, I, I, P, P, I, F, P, P, ctypes.c_size_t, P, P]),
+        "fp8attn_kv_keep_path": (I, [P, P, I64, I64, I64, I, I, I, I, I, P, I64, I, P, P, I, P,
+                                     I64, I, P, P, P]),
         "fp8attn_apply_margin": (I, [P, I64, F, P]),
         "fp8attn_scale_map_parse": (I, [ctypes.c_char_p, ctypes.c_size_t, F, I, P, P,
                                         ctypes.POINTER(I)]),
@@ -401,6 +413,22 @@ class Context:
             raise FP8AttnError(1, "fp8attn_quant_scale_ptr")
         return int(p)
 
+    def static_quant_scale_ptr(self, layer: int) -> int:
+        """Device pointer to the layer's static {qs_q, qs_k, qs_v}: the scale
+        argument of :func:`kv_write` (a cache outlives the current scales)."""
+        p = lib().fp8attn_static_quant_scale_ptr(self._h, layer)
+        if not p:
+            raise FP8AttnError(1, "fp8attn_static_quant_scale_ptr")
+        return int(p)
+
+    def static_descale_ptr(self, layer: int) -> int:
+        """Device pointer to the layer's static {ds_q, ds_k, ds_v}: the descale
+        argument of :func:`kv_tree_fwd`."""
+        p = lib().fp8attn_static_descale_ptr(self._h, layer)
+        if not p:
+            raise FP8AttnError(1, "fp8attn_static_descale_ptr")
+        return int(p)
+
     def get_ring_state(self, layer: int, stream=None) -> Tuple[np.ndarray, np.ndarray]:
         slots = np.zeros((3, RING_LENGTH), dtype=np.float32)
         meta = np.zeros((3, 2), dtype=np.uint32)
@@ -525,6 +553,256 @@ def read_error_word(error: torch.Tensor, stream=None) -> int:
     _require_cuda(error, "error")
     return int(lib().fp8attn_read_error_word(_ptr(error),
                                              ctypes.c_void_p(_stream(stream, error.device))))
+
+
+# ---------------------------------------------------------------------------
+# paged KV cache
+# ---------------------------------------------------------------------------
+
+def _launch_on(stream, device):
+    """(handle, context manager): the stream of a call and a context in which
+    the call's device is current and torch allocates on that stream, so that
+    neither its outputs nor its workspace are memory that another stream's
+    pending work still uses."""
+    if stream is None:
+        if device.index == torch.cuda.current_device():
+            return torch.cuda.current_stream(device).cuda_stream, contextlib.nullcontext()
+        return torch.cuda.current_stream(device).cuda_stream, torch.cuda.device(device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) \
+            else torch.cuda.default_stream(device)
+    if stream.device != device:
+        raise ValueError(f"the stream is not one of {device}")
+    return stream.cuda_stream, torch.cuda.stream(stream)
+
+
+def _int32(t, name: str, device, numel: Optional[int] = None) -> int:
+    """Pointer of a contiguous int32 tensor on ``device`` (of ``numel`` elements)."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device:
+        raise ValueError(f"{name} must be an int32 tensor on {device}")
+    if not t.is_contiguous() or (numel is not None and t.numel() != numel):
+        raise ValueError(f"{name} must be contiguous" +
+                         (f" and hold {numel} elements" if numel is not None else ""))
+    return t.data_ptr()
+
+
+def _block_tables(t, rows: int, device):
+    """(pointer, row stride, width) of int32 block tables [rows, width]."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device:
+        raise ValueError(f"block_tables must be an int32 tensor on {device}")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] < 1 or \
+            (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"block_tables must be [{rows}, width >= 1] with contiguous rows")
+    return t.data_ptr(), t.stride(0), t.shape[1]
+
+
+def _paged_cache(k_cache, v_cache):
+    """(pages, page_size, heads, strides, device) of a paged cache: uint8 (E4M3
+    codes) or bf16 [pages, page_size, heads, 128] views of any strides with
+    the channel contiguous."""
+    _require_cuda(k_cache, "k_cache")
+    _require_cuda(v_cache, "v_cache")
+    shape, strides = k_cache.shape, k_cache.stride()
+    if k_cache.dtype not in (torch.uint8, torch.bfloat16) or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must both be uint8 (E4M3 codes) or bfloat16")
+    if v_cache.shape != shape or v_cache.stride() != strides or v_cache.device != k_cache.device:
+        raise ValueError("k_cache and v_cache must share shape, strides and device")
+    if len(shape) != 4 or shape[3] != HEAD_DIM or strides[3] != 1:
+        raise ValueError("a cache is [pages, page_size, heads, 128] with contiguous channels")
+    return shape[0], shape[1], shape[2], strides, k_cache.device
+
+
+def _scale3(scale, name: str, fp8: bool, device) -> int:
+    """Device pointer of three fp32 scales (an int pointer or a tensor), which an
+    E4M3 cache needs and a bf16 cache does not have."""
+    if (scale is not None) != fp8:
+        raise ValueError(f"{name} is needed for an E4M3 cache" if fp8
+                         else f"a bf16 cache takes no {name}")
+    if scale is None:
+        return 0
+    if isinstance(scale, torch.Tensor):
+        if scale.dtype != torch.float32 or scale.numel() != 3 or not scale.is_contiguous() or \
+                scale.device != device:
+            raise ValueError(f"{name} must be 3 contiguous fp32 values on {device}")
+        return scale.data_ptr()
+    return int(scale)
+
+
+def _error_ptr(error, device) -> int:
+    return 0 if error is None else _int32(error, "error", device, 1)
+
+
+def kv_assign_pages(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_tables: torch.Tensor,
+                    owned: torch.Tensor, free_pages: torch.Tensor, pool: torch.Tensor,
+                    page_size: int, max_tokens: int, *, out=None,
+                    error: Optional[torch.Tensor] = None, stream=None
+                    ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Block tables and the slot map of one step, built on the device from the
+    requests' lengths.  Row b holds ``seq_lens[b]`` tokens after the step, the
+    last ``new_lens[b]`` of which are new; rows that need more pages than the
+    ``owned[b]`` they hold take them from the pool, rows that need fewer give
+    their last ones back (length 0: a request that ended).  ``block_tables``
+    [rows, width], ``owned`` [rows], ``free_pages`` [num_pages] and ``pool``
+    ({free pages, 0}) are int32 and updated in place.  Returns (cu_new int32
+    [rows + 1], slots int64 [max_tokens], positions int32 [max_tokens]); slots
+    behind the last new token are -1, which :func:`kv_write` skips.  Too few
+    free pages or inconsistent lengths change nothing and set ``error`` (see
+    fp8attn_kv_assign_pages in fp8attn.h)."""
+    _require_cuda(seq_lens, "seq_lens")
+    dev, rows = seq_lens.device, seq_lens.numel()
+    max_tokens = int(max_tokens)
+    if max_tokens < 0:
+        raise ValueError("max_tokens must not be negative")
+    tables, table_stride, width = _block_tables(block_tables, rows, dev)
+    args = (_int32(seq_lens, "seq_lens", dev), _int32(new_lens, "new_lens", dev, rows), rows,
+            int(page_size), tables, table_stride, width, _int32(owned, "owned", dev, rows),
+            _int32(free_pages, "free_pages", dev), free_pages.numel(),
+            _int32(pool, "pool", dev, 2), max_tokens)
+    err = _error_ptr(error, dev)
+    handle, on = _launch_on(stream, dev)
+    with on:
+        if out is None:
+            # one allocation: slots, positions, cu (slots and positions 16-byte aligned)
+            n8, n4 = 8 * max_tokens + 15 & ~15, 4 * max_tokens + 15 & ~15
+            buf = torch.empty(n8 + n4 + 4 * rows + 4, dtype=torch.uint8, device=dev)
+            slots = buf[:8 * max_tokens].view(torch.int64)
+            positions = buf[n8:n8 + 4 * max_tokens].view(torch.int32)
+            cu = buf[n8 + n4:].view(torch.int32)
+        else:
+            cu, slots, positions = out
+            _check_out(cu, "cu_new", torch.int32, rows + 1, dev)
+            _check_out(slots, "slots", torch.int64, max_tokens, dev)
+            _check_out(positions, "positions", torch.int32, max_tokens, dev)
+        if rows == 0:
+            cu.zero_()
+        _check(lib().fp8attn_kv_assign_pages(*args, cu.data_ptr(), slots.data_ptr(),
+                                             positions.data_ptr(), err, handle),
+               "fp8attn_kv_assign_pages")
+    return cu, slots, positions
+
+
+def kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor,
+             v_cache: torch.Tensor, quant_scale=None, *, error: Optional[torch.Tensor] = None,
+             stream=None) -> None:
+    """Write the K and V of new tokens (bf16 [T, H, 128], or strided views such
+    as slices of a fused [T, 3, H, 128] projection) into their cache slots
+    (int64 [T]; negative: skipped).  uint8 caches receive E4M3 codes of
+    fl32(x * scale), with ``quant_scale`` a device pointer (e.g.
+    ``Context.static_quant_scale_ptr(layer)``) or a 3-element fp32 tensor
+    {qs_q, qs_k, qs_v}; bf16 caches take no scale."""
+    pages, page_size, heads, strides, dev = _paged_cache(k_cache, v_cache)
+    for name, t in (("k", k), ("v", v)):
+        _require_cuda(t, name)
+        if t.dtype != torch.bfloat16 or t.device != dev:
+            raise ValueError(f"{name} must be bfloat16 on {dev}")
+    if k.shape != v.shape or k.stride() != v.stride():
+        raise ValueError("k and v must share shape and strides")
+    if k.dim() != 3 or k.shape[1] != heads or k.shape[2] != HEAD_DIM or k.stride(2) != 1:
+        raise ValueError(f"k and v must be [T, {heads}, 128] with contiguous channels")
+    T = k.shape[0]
+    if not isinstance(slots, torch.Tensor) or slots.dtype != torch.int64 or \
+            slots.device != dev or slots.shape != (T,) or not slots.is_contiguous():
+        raise ValueError(f"slots must be a contiguous int64 [{T}] tensor on {dev}")
+    scale = _scale3(quant_scale, "quant_scale", k_cache.dtype == torch.uint8, dev)
+    # the stride of a dimension of size one says nothing
+    tok_stride = k.stride(0) if T > 1 else heads * HEAD_DIM
+    head_stride = k.stride(1) if heads > 1 else HEAD_DIM
+    err = _error_ptr(error, dev)
+    handle, on = _launch_on(stream, dev)
+    with on:
+        _check(lib().fp8attn_kv_write(
+            k.data_ptr(), v.data_ptr(), tok_stride, head_stride, slots.data_ptr(), T, heads,
+            HEAD_DIM, k_cache.data_ptr(), v_cache.data_ptr(), strides[0], strides[1], strides[2],
+            pages, page_size, scale, err, handle), "fp8attn_kv_write")
+
+
+def kv_tree_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                block_tables: torch.Tensor, seq_lens: torch.Tensor, cu_q: torch.Tensor,
+                max_q_len: int, max_seqlen: int, descale=None,
+                tree_mask: Optional[torch.Tensor] = None, softmax_scale: float = 0.0, *,
+                out: Optional[torch.Tensor] = None, error: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+    """Attention of new tokens over the paged cache: a drafted tree, a chain or
+    a single token per request.  Request b's queries, rows ``cu_q[b]`` to
+    ``cu_q[b + 1]`` of ``q`` (bf16 [T, heads, 128], strided views allowed), are
+    the last tokens of its ``seq_lens[b]`` (at most ``max_q_len`` and
+    ``max_seqlen``), whose K and V are in the cache already.  A query sees all
+    positions before the request's queries, and of those the ones whose bits
+    its row of ``tree_mask`` (int64 [T, words], bit m % 64 of word m / 64 for
+    query m of the request) sets; without a mask, itself and the earlier ones.
+    ``descale``: device pointer (e.g. ``Context.static_descale_ptr(layer)``) or
+    a 3-element fp32 tensor {ds_q, ds_k, ds_v} for a uint8 (E4M3) cache; a
+    bf16 cache takes none.  Returns bf16 [T, heads, 128] (a query that sees
+    nothing: 0; rows of no request in a given ``out`` stay as they are)."""
+    pages, page_size, kv_heads, strides, dev = _paged_cache(k_cache, v_cache)
+    _require_cuda(q, "q")
+    if q.dtype != torch.bfloat16 or q.device != dev:
+        raise ValueError(f"q must be bfloat16 on {dev}")
+    if q.dim() != 3 or q.shape[2] != HEAD_DIM or q.stride(2) != 1:
+        raise ValueError("q must be [T, heads, 128] with contiguous channels")
+    T, heads = q.shape[0], q.shape[1]
+    if heads < 1 or kv_heads < 1 or heads % kv_heads:
+        raise ValueError(f"{heads} query heads are no multiple of {kv_heads} KV heads")
+    _require_cuda(seq_lens, "seq_lens")
+    rows = seq_lens.numel()
+    tables, table_stride, width = _block_tables(block_tables, rows, dev)
+    seq, cu = _int32(seq_lens, "seq_lens", dev), _int32(cu_q, "cu_q", dev, rows + 1)
+    mask, words = 0, 0
+    if tree_mask is not None:
+        if not isinstance(tree_mask, torch.Tensor) or tree_mask.dtype != torch.int64 or \
+                tree_mask.device != dev or tree_mask.dim() != 2 or tree_mask.shape[0] != T or \
+                tree_mask.shape[1] < 1 or not tree_mask.is_contiguous():
+            raise ValueError(f"tree_mask must be a contiguous int64 [{T}, words] tensor on {dev}")
+        mask, words = tree_mask.data_ptr(), tree_mask.shape[1]
+    scale = _scale3(descale, "descale", k_cache.dtype == torch.uint8, dev)
+    tok_stride = q.stride(0) if T > 1 else heads * HEAD_DIM
+    head_stride = q.stride(1) if heads > 1 else HEAD_DIM
+    max_q_len, max_seqlen = int(max_q_len), int(max_seqlen)
+    err = _error_ptr(error, dev)
+    L = lib()
+    need = L.fp8attn_kv_tree_workspace_bytes(rows, max_q_len, max_seqlen, heads, kv_heads)
+    handle, on = _launch_on(stream, dev)
+    with on:
+        if out is None:
+            out = torch.empty((T, heads, HEAD_DIM), dtype=torch.bfloat16, device=dev)
+        else:
+            _check_out(out, "out", torch.bfloat16, T * heads * HEAD_DIM, dev)
+        work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        _check(L.fp8attn_kv_tree_fwd(
+            q.data_ptr(), tok_stride, head_stride, k_cache.data_ptr(), v_cache.data_ptr(),
+            strides[0], strides[1], strides[2], pages, page_size, tables, table_stride, width,
+            seq, cu, rows, max_q_len, max_seqlen, T, heads, kv_heads, HEAD_DIM, scale, mask,
+            words, float(softmax_scale), out.data_ptr(),
+            0 if work is None else work.data_ptr(), need, err, handle), "fp8attn_kv_tree_fwd")
+    return out
+
+
+def kv_keep_path(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                 seq_lens: torch.Tensor, cu_q: torch.Tensor, paths: torch.Tensor,
+                 keep_lens: torch.Tensor, *, error: Optional[torch.Tensor] = None,
+                 stream=None) -> None:
+    """After verification of drafted trees: request b's accepted nodes
+    ``paths[b, :keep_lens[b]]`` (int32 [rows, depth], rising node indices) of
+    its n_b = ``cu_q[b + 1] - cu_q[b]`` nodes, the last n_b of ``seq_lens[b]``
+    positions, move to nodes 0, 1, ... of the cache, in place.  The request
+    then holds seq_lens[b] - n_b + keep_lens[b] tokens."""
+    pages, page_size, heads, strides, dev = _paged_cache(k_cache, v_cache)
+    _require_cuda(seq_lens, "seq_lens")
+    rows = seq_lens.numel()
+    tables, table_stride, width = _block_tables(block_tables, rows, dev)
+    if not isinstance(paths, torch.Tensor) or paths.dtype != torch.int32 or \
+            paths.device != dev or paths.dim() != 2 or paths.shape[0] != rows or \
+            (paths.shape[1] > 1 and paths.stride(1) != 1):
+        raise ValueError(f"paths must be an int32 [{rows}, depth] tensor on {dev}")
+    args = (_int32(seq_lens, "seq_lens", dev), _int32(cu_q, "cu_q", dev, rows + 1), rows,
+            paths.data_ptr(), paths.stride(0), paths.shape[1],
+            _int32(keep_lens, "keep_lens", dev, rows), _error_ptr(error, dev))
+    handle, on = _launch_on(stream, dev)
+    with on:
+        _check(lib().fp8attn_kv_keep_path(
+            k_cache.data_ptr(), v_cache.data_ptr(), strides[0], strides[1], strides[2], pages,
+            page_size, k_cache.element_size(), heads, HEAD_DIM, tables, table_stride, width,
+            *args, handle), "fp8attn_kv_keep_path")
 
 
 # ---------------------------------------------------------------------------

@@ -39,6 +39,7 @@ inline bool layer_ok(const fp8attn_ctx* c, int layer) {
 fp8attn_status status_of_bits(uint32_t bits) {
   if (bits & kErrTimeout) return FP8ATTN_ERR_TIMEOUT;
   if (bits & kErrSeqlens) return FP8ATTN_ERR_SEQLENS;
+  if (bits & kErrPages) return FP8ATTN_ERR_PAGES;
   if (bits & kErrNonfinite) return FP8ATTN_ERR_NONFINITE;
   return FP8ATTN_OK;
 }
@@ -106,6 +107,39 @@ fp8attn_status run_attention(const void* q, const void* k, const void* v, const 
   return FP8ATTN_OK;
 }
 
+// log2 of a page size the paged cache supports (8 to 1024 slots), or -1
+int page_log2_of(int page_size) {
+  for (int l = 3; l <= 10; ++l)
+    if (page_size == 1 << l) return l;
+  return -1;
+}
+
+// Shared checks of a paged cache.  The strides of a dimension of size one do
+// not matter; they are replaced by ones that the kernels accept.
+fp8attn_status check_cache(const void* k, const void* v, int64_t page_stride, int64_t slot_stride,
+                           int64_t head_stride, int num_pages, int page_size, int heads,
+                           int head_dim, bool fp8, PagedCache* out) {
+  if (num_pages < 1 || page_size < 1 || heads < 1) return FP8ATTN_ERR_INVALID;
+  if (head_dim != kHeadDim || page_log2_of(page_size) < 0) return FP8ATTN_ERR_UNSUPPORTED;
+  if (!k || !v) return FP8ATTN_ERR_INVALID;
+  if (num_pages == 1) page_stride = kHeadDim;
+  if (heads == 1) head_stride = kHeadDim;
+  const int64_t unit = fp8 ? 16 : 8;   // elements of 16 bytes
+  for (int64_t s : {page_stride, slot_stride, head_stride})
+    if (s < kHeadDim || s % unit || s >= int64_t{1} << 38) return FP8ATTN_ERR_UNSUPPORTED;
+  if (!aligned(k, 16) || !aligned(v, 16)) return FP8ATTN_ERR_UNSUPPORTED;
+  out->k = const_cast<void*>(k);
+  out->v = const_cast<void*>(v);
+  out->page_stride = page_stride;
+  out->slot_stride = slot_stride;
+  out->head_stride = head_stride;
+  out->num_pages = num_pages;
+  out->page_log2 = page_log2_of(page_size);
+  out->heads = heads;
+  out->fp8 = fp8;
+  return FP8ATTN_OK;
+}
+
 }  // namespace
 
 void fp8attn::note_launch() { g_launches.fetch_add(1); }
@@ -121,6 +155,7 @@ const char* fp8attn_status_string(int status) {
     case FP8ATTN_ERR_UNSUPPORTED: return "unsupported configuration";
     case FP8ATTN_ERR_NONFINITE: return "non-finite amax";
     case FP8ATTN_ERR_SEQLENS: return "inconsistent cu_seqlens";
+    case FP8ATTN_ERR_PAGES: return "page outside the cache, or too few free pages";
     default: return "unknown status";
   }
 }
@@ -641,6 +676,197 @@ fp8attn_status fp8attn_regroup_heads(const void* d_src, void* d_dst, int64_t tok
   const cudaError_t e = launch_regroup_heads(d_src, d_dst, tokens, num_heads, groups, head_bytes,
                                              to_groups, as_stream(stream));
   if (e != cudaSuccess) return FP8ATTN_ERR_CUDA;
+  g_launches.fetch_add(1);
+  return FP8ATTN_OK;
+}
+
+const float* fp8attn_static_quant_scale_ptr(fp8attn_ctx* ctx, int layer) {
+  if (!layer_ok(ctx, layer) || !ctx->has_static[layer]) return nullptr;
+  return ctx->ls[layer].static_qs;
+}
+
+const float* fp8attn_static_descale_ptr(fp8attn_ctx* ctx, int layer) {
+  if (!layer_ok(ctx, layer) || !ctx->has_static[layer]) return nullptr;
+  return ctx->ls[layer].static_ds;
+}
+
+fp8attn_status fp8attn_kv_assign_pages(const int32_t* d_seq_lens, const int32_t* d_new_lens,
+                                       int rows, int page_size, int32_t* d_block_tables,
+                                       int64_t table_stride, int table_width, int32_t* d_owned,
+                                       int32_t* d_free_pages, int num_pages, int32_t* d_pool,
+                                       int64_t max_tokens, int32_t* d_cu_new, int64_t* d_slots,
+                                       int32_t* d_positions, int32_t* d_error, void* stream) {
+  if (rows < 0 || num_pages < 1 || table_width < 1 || max_tokens < 0 || page_size < 1)
+    return FP8ATTN_ERR_INVALID;
+  const int page_log2 = page_log2_of(page_size);
+  if (page_log2 < 0 || rows > kMaxPageRows || num_pages >= 1 << 30 || max_tokens > 0x7FFFFFFFLL)
+    return FP8ATTN_ERR_UNSUPPORTED;
+  if (rows == 0) return max_tokens == 0 ? FP8ATTN_OK : FP8ATTN_ERR_INVALID;
+  if (rows > 1 && table_stride < table_width) return FP8ATTN_ERR_INVALID;
+  if (!d_seq_lens || !d_new_lens || !d_block_tables || !d_owned || !d_free_pages || !d_pool ||
+      !d_cu_new || (max_tokens > 0 && (!d_slots || !d_positions)))
+    return FP8ATTN_ERR_INVALID;
+  if (!aligned(d_slots, 16) || !aligned(d_positions, 16)) return FP8ATTN_ERR_INVALID;
+  AssignPagesLaunch p;
+  p.seq = d_seq_lens;
+  p.fresh = d_new_lens;
+  p.tables = d_block_tables;
+  p.table_stride = table_stride;
+  p.width = table_width;
+  p.owned = d_owned;
+  p.free_pages = d_free_pages;
+  p.num_pages = num_pages;
+  p.pool = d_pool;
+  p.rows = rows;
+  p.page_log2 = page_log2;
+  p.max_tokens = static_cast<int>(max_tokens);
+  p.cu = d_cu_new;
+  p.slots = d_slots;
+  p.positions = d_positions;
+  p.err = d_error;
+  if (launch_assign_pages(p, as_stream(stream)) != cudaSuccess) return FP8ATTN_ERR_CUDA;
+  g_launches.fetch_add(1);
+  return FP8ATTN_OK;
+}
+
+fp8attn_status fp8attn_kv_write(const void* k, const void* v, int64_t tok_stride,
+                                int64_t head_stride, const int64_t* d_slots, int64_t tokens,
+                                int num_kv_heads, int head_dim, void* k_cache, void* v_cache,
+                                int64_t page_stride, int64_t slot_stride,
+                                int64_t cache_head_stride, int num_pages, int page_size,
+                                const float* d_quant_scale_qkv, int32_t* d_error, void* stream) {
+  if (tokens < 0) return FP8ATTN_ERR_INVALID;
+  KvWriteLaunch p;
+  const fp8attn_status st =
+      check_cache(k_cache, v_cache, page_stride, slot_stride, cache_head_stride, num_pages,
+                  page_size, num_kv_heads, head_dim, d_quant_scale_qkv != nullptr, &p.cache);
+  if (st != FP8ATTN_OK || tokens == 0) return st;
+  if (!k || !v || !d_slots) return FP8ATTN_ERR_INVALID;
+  if (tok_stride <= 0 || head_stride <= 0 || (tok_stride % 8) || (head_stride % 8) ||
+      !aligned(k, 16) || !aligned(v, 16) || !aligned(d_slots, 8) ||
+      tokens > 0x7FFFFFFFLL / num_kv_heads)
+    return FP8ATTN_ERR_UNSUPPORTED;
+  p.k = k;
+  p.v = v;
+  p.tok_stride = tok_stride;
+  p.head_stride = head_stride;
+  p.slots = d_slots;
+  p.tokens = tokens;
+  p.qs = d_quant_scale_qkv;
+  p.err = d_error;
+  if (launch_kv_write(p, as_stream(stream)) != cudaSuccess) return FP8ATTN_ERR_CUDA;
+  g_launches.fetch_add(1);
+  return FP8ATTN_OK;
+}
+
+size_t fp8attn_kv_tree_workspace_bytes(int rows, int max_q_len, int max_seqlen, int num_heads,
+                                       int num_kv_heads) {
+  if (rows < 1 || max_q_len < 1 || max_seqlen < 1 || num_kv_heads < 1 || num_heads < 1 ||
+      num_heads % num_kv_heads || rows > kMaxTreeRows)
+    return 0;
+  return kv_tree_workspace_bytes(rows, max_q_len, max_seqlen, num_heads, num_kv_heads);
+}
+
+fp8attn_status fp8attn_kv_tree_fwd(const void* q, int64_t q_tok_stride, int64_t q_head_stride,
+                                   const void* k_cache, const void* v_cache,
+                                   int64_t page_stride, int64_t slot_stride,
+                                   int64_t cache_head_stride, int num_pages, int page_size,
+                                   const int32_t* d_block_tables, int64_t table_stride,
+                                   int table_width, const int32_t* d_seq_lens,
+                                   const int32_t* d_cu_q, int rows, int max_q_len,
+                                   int max_seqlen, int64_t total_q, int num_heads,
+                                   int num_kv_heads, int head_dim, const float* d_descale_qkv,
+                                   const int64_t* d_tree_mask, int mask_words,
+                                   float softmax_scale, void* out, void* workspace,
+                                   size_t workspace_bytes, int32_t* d_error, void* stream) {
+  if (rows < 0 || max_q_len < 0 || max_seqlen < 0 || total_q < 0 || num_heads < 1 ||
+      num_kv_heads < 1 || num_heads % num_kv_heads || table_width < 1 ||
+      (d_tree_mask && mask_words < 1))
+    return FP8ATTN_ERR_INVALID;
+  if (!(softmax_scale >= 0.0f) || std::isinf(softmax_scale)) return FP8ATTN_ERR_INVALID;
+  KvTreeLaunch p;
+  const fp8attn_status st =
+      check_cache(k_cache, v_cache, page_stride, slot_stride, cache_head_stride, num_pages,
+                  page_size, num_kv_heads, head_dim, d_descale_qkv != nullptr, &p.cache);
+  if (st != FP8ATTN_OK) return st;
+  if (rows > kMaxTreeRows) return FP8ATTN_ERR_UNSUPPORTED;
+  if (rows == 0 || total_q == 0) return FP8ATTN_OK;
+  if (rows > 1 && table_stride < table_width) return FP8ATTN_ERR_INVALID;
+  if (!q || !out || !d_block_tables || !d_seq_lens || !d_cu_q) return FP8ATTN_ERR_INVALID;
+  if (q_tok_stride <= 0 || q_head_stride <= 0 || (q_tok_stride % 8) || (q_head_stride % 8) ||
+      !aligned(q, 16) || !aligned(out, 16) || !aligned(d_tree_mask, 8) ||
+      total_q > 0x7FFFFFFFLL / num_heads ||
+      static_cast<int64_t>(max_q_len) * (num_heads / num_kv_heads) > 0x7FFFFFFFLL)
+    return FP8ATTN_ERR_UNSUPPORTED;
+  // no request has more queries than there are, nor tokens than its table holds
+  if (max_q_len > total_q) max_q_len = static_cast<int>(total_q);
+  const int64_t held = static_cast<int64_t>(table_width) * page_size;
+  if (max_seqlen > held) max_seqlen = static_cast<int>(held);
+  const size_t need =
+      max_q_len && max_seqlen
+          ? kv_tree_workspace_bytes(rows, max_q_len, max_seqlen, num_heads, num_kv_heads)
+          : 0;
+  if (kv_tree_max_tiles(rows, max_q_len, max_seqlen, num_heads, num_kv_heads) > 0x7FFFFFFFLL)
+    return FP8ATTN_ERR_UNSUPPORTED;
+  if (need > workspace_bytes || (need && !workspace)) return FP8ATTN_ERR_INVALID;
+  if (!aligned(workspace, 16)) return FP8ATTN_ERR_UNSUPPORTED;
+  p.q = q;
+  p.q_tok_stride = q_tok_stride;
+  p.q_head_stride = q_head_stride;
+  p.tables = d_block_tables;
+  p.table_stride = table_stride;
+  p.width = table_width;
+  p.seq = d_seq_lens;
+  p.cu = d_cu_q;
+  p.rows = rows;
+  p.max_q = max_q_len;
+  p.max_seqlen = max_seqlen;
+  p.total_q = total_q;
+  p.heads = num_heads;
+  p.descale = d_descale_qkv;
+  p.mask = d_tree_mask;
+  p.mask_words = mask_words;
+  p.softmax_scale = softmax_scale == 0.0f ? 1.0f / std::sqrt(static_cast<float>(head_dim))
+                                          : softmax_scale;
+  p.out = out;
+  p.workspace = workspace;
+  p.err = d_error;
+  if (launch_kv_tree(p, as_stream(stream)) != cudaSuccess) return FP8ATTN_ERR_CUDA;
+  g_launches.fetch_add(1);
+  return FP8ATTN_OK;
+}
+
+fp8attn_status fp8attn_kv_keep_path(void* k_cache, void* v_cache, int64_t page_stride,
+                                    int64_t slot_stride, int64_t cache_head_stride, int num_pages,
+                                    int page_size, int elem_bytes, int num_kv_heads, int head_dim,
+                                    const int32_t* d_block_tables, int64_t table_stride,
+                                    int table_width, const int32_t* d_seq_lens,
+                                    const int32_t* d_cu_q, int rows, const int32_t* d_paths,
+                                    int64_t path_stride, int depth, const int32_t* d_keep_lens,
+                                    int32_t* d_error, void* stream) {
+  if (rows < 0 || depth < 0 || table_width < 1 || (elem_bytes != 1 && elem_bytes != 2))
+    return FP8ATTN_ERR_INVALID;
+  KvKeepLaunch p;
+  const fp8attn_status st =
+      check_cache(k_cache, v_cache, page_stride, slot_stride, cache_head_stride, num_pages,
+                  page_size, num_kv_heads, head_dim, elem_bytes == 1, &p.cache);
+  if (st != FP8ATTN_OK || rows == 0 || depth == 0) return st;
+  if (num_kv_heads > 1 << 18) return FP8ATTN_ERR_UNSUPPORTED;
+  if (rows > 1 && (table_stride < table_width || path_stride < depth)) return FP8ATTN_ERR_INVALID;
+  if (!d_block_tables || !d_seq_lens || !d_cu_q || !d_paths || !d_keep_lens)
+    return FP8ATTN_ERR_INVALID;
+  p.tables = d_block_tables;
+  p.table_stride = table_stride;
+  p.width = table_width;
+  p.seq = d_seq_lens;
+  p.cu = d_cu_q;
+  p.rows = rows;
+  p.paths = d_paths;
+  p.path_stride = path_stride;
+  p.depth = depth;
+  p.keep = d_keep_lens;
+  p.err = d_error;
+  if (launch_kv_keep(p, as_stream(stream)) != cudaSuccess) return FP8ATTN_ERR_CUDA;
   g_launches.fetch_add(1);
   return FP8ATTN_OK;
 }

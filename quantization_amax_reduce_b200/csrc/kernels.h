@@ -83,4 +83,98 @@ void note_launch();
 cudaError_t launch_regroup_heads(const void* src, void* dst, int64_t tokens, int heads,
                                  int groups, int head_bytes, int to_groups, cudaStream_t stream);
 
+// A paged KV cache: element (slot, head, channel) of K or V at
+// base + (slot >> page_log2) * page_stride + (slot & (page - 1)) * slot_stride
+// + head * head_stride + channel (elements of 1 byte for fp8, else 2).
+struct PagedCache {
+  void* k;
+  void* v;
+  int64_t page_stride, slot_stride, head_stride;
+  int num_pages, page_log2, heads;
+  bool fp8;
+};
+
+// Page assignment: tables [rows][width] (row stride table_stride), owned
+// [rows], free_pages [num_pages], pool {free count, 0 between calls};
+// cu [rows + 1], slots and positions [max_tokens] (16-byte aligned).
+struct AssignPagesLaunch {
+  const int32_t* seq;
+  const int32_t* fresh;
+  int32_t* tables;
+  int64_t table_stride;
+  int width;
+  int32_t* owned;
+  int32_t* free_pages;
+  int num_pages;
+  int32_t* pool;
+  int rows, page_log2, max_tokens;
+  int32_t* cu;
+  int64_t* slots;
+  int32_t* positions;
+  int32_t* err;
+};
+
+constexpr int kMaxPageRows = 16384;   // three prefix sums in shared memory
+
+cudaError_t launch_assign_pages(const AssignPagesLaunch& p, cudaStream_t stream);
+
+struct KvWriteLaunch {
+  const void* k;                 // bf16 sources
+  const void* v;
+  int64_t tok_stride, head_stride;
+  const int64_t* slots;
+  int64_t tokens;                // tokens * heads < 2^31
+  PagedCache cache;
+  const float* qs;               // device {qs_q, qs_k, qs_v} (fp8 only)
+  int32_t* err;
+};
+
+cudaError_t launch_kv_write(const KvWriteLaunch& p, cudaStream_t stream);
+
+struct KvKeepLaunch {
+  PagedCache cache;
+  const int32_t* tables;
+  int64_t table_stride;
+  int width;
+  const int32_t* seq;
+  const int32_t* cu;
+  int rows;
+  const int32_t* paths;
+  int64_t path_stride;
+  int depth;
+  const int32_t* keep;
+  int32_t* err;
+};
+
+cudaError_t launch_kv_keep(const KvKeepLaunch& p, cudaStream_t stream);
+
+struct KvTreeLaunch {
+  const void* q;                 // bf16
+  int64_t q_tok_stride, q_head_stride;
+  PagedCache cache;
+  const int32_t* tables;
+  int64_t table_stride;
+  int width;
+  const int32_t* seq;
+  const int32_t* cu;
+  int rows, max_q, max_seqlen;
+  int64_t total_q;
+  int heads;                     // query heads, a multiple of cache.heads
+  const float* descale;          // device {ds_q, ds_k, ds_v} (fp8 only)
+  const int64_t* mask;           // [total_q][mask_words] or null (chains)
+  int mask_words;
+  float softmax_scale;
+  void* out;                     // bf16 [total_q, heads, 128]
+  void* workspace;
+  int32_t* err;
+};
+
+constexpr int kMaxTreeRows = 2048;    // a prefix sum in shared memory
+
+// Work items (128-key tiles of a request's KV heads and query row tiles) that
+// lengths up to the given ones can come to.
+int64_t kv_tree_max_tiles(int rows, int max_q, int max_seqlen, int heads, int kv_heads);
+size_t kv_tree_workspace_bytes(int rows, int max_q, int max_seqlen, int heads, int kv_heads);
+cudaError_t launch_kv_tree(const KvTreeLaunch& p, cudaStream_t stream);
+
 }  // namespace fp8attn

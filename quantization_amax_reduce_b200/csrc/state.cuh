@@ -17,6 +17,7 @@ constexpr float kE4M3Max = 448.0f;
 constexpr uint32_t kErrTimeout = 1u;
 constexpr uint32_t kErrNonfinite = 2u;
 constexpr uint32_t kErrSeqlens = 4u;
+constexpr uint32_t kErrPages = 8u;
 
 struct GlobalState {
   uint32_t amax_bits[4];   // per-call |x| max as bf16 magnitude bits (q, k, v)

@@ -1,0 +1,155 @@
+"""The paged KV cache entry points refuse what they cannot compute on the host,
+before any CUDA call, and do nothing for empty calls (no GPU needed)."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+P = ctypes.c_void_p
+OK, INVALID, UNSUPPORTED = 0, 1, 4
+
+
+@pytest.fixture(scope="module")
+def L():
+    from quantization_amax_reduce_b200 import build
+    build.build()
+    import quantization_amax_reduce_b200 as qar
+    return qar.lib()
+
+
+def call(fn, base, **change):
+    args = dict(base)
+    assert set(change) <= set(args)
+    args.update(change)
+    return fn(*args.values())
+
+
+def test_assign_pages_refusals(L):
+    base = dict(seq=P(16), new=P(16), rows=4, page=16, tables=P(16), stride=8, width=8,
+                owned=P(16), free=P(16), num=32, pool=P(16), tokens=64, cu=P(16), slots=P(16),
+                pos=P(16), err=None, stream=None)
+    f = L.fp8attn_kv_assign_pages
+    for change in (dict(rows=-1), dict(num=0), dict(width=0), dict(tokens=-1), dict(page=0),
+                   dict(stride=7), dict(seq=None), dict(new=None), dict(tables=None),
+                   dict(owned=None), dict(free=None), dict(pool=None), dict(cu=None),
+                   dict(slots=None), dict(pos=None), dict(slots=P(8)), dict(pos=P(8)),
+                   dict(rows=0)):
+        assert call(f, base, **change) == INVALID, change
+    for change in (dict(page=4), dict(page=24), dict(page=2048), dict(rows=16385),
+                   dict(num=1 << 30), dict(tokens=1 << 31)):
+        assert call(f, base, **change) == UNSUPPORTED, change
+    assert call(f, base, rows=0, tokens=0) == OK
+
+
+WRITE = dict(k=P(16), v=P(16), tok=1024, head=128, slots=P(16), tokens=5, heads=8, dim=128,
+             kc=P(16), vc=P(16), page_stride=16384, slot_stride=1024, chead=128, num=32, page=16,
+             qs=P(16), err=None, stream=None)
+
+
+def test_write_refusals(L):
+    f = L.fp8attn_kv_write
+    for change in (dict(tokens=-1), dict(num=0), dict(heads=0), dict(page=0), dict(k=None),
+                   dict(v=None), dict(slots=None), dict(kc=None), dict(vc=None)):
+        assert call(f, WRITE, **change) == INVALID, change
+    for change in (dict(dim=64), dict(page=12), dict(tok=1001), dict(head=0), dict(k=P(8)),
+                   dict(kc=P(8)), dict(vc=P(24)), dict(slots=P(4)), dict(page_stride=16392),
+                   dict(slot_stride=64), dict(chead=136), dict(page_stride=1 << 38),
+                   dict(tokens=1 << 28)):
+        assert call(f, WRITE, **change) == UNSUPPORTED, change
+    # 8-channel strides are 16 bytes of bf16, but not of E4M3
+    assert call(f, WRITE, chead=136, qs=None, tokens=0) == OK
+    assert call(f, WRITE, tokens=0, k=None, v=None, slots=None) == OK
+
+
+TREE = dict(q=P(16), qt=4096, qh=128, kc=P(16), vc=P(16), page_stride=16384, slot_stride=1024,
+            chead=128, num=32, page=16, tables=P(16), stride=8, width=8, seq=P(16), cu=P(16),
+            rows=3, max_q=4, max_seq=128, total=12, heads=32, kv=8, dim=128, ds=P(16),
+            mask=P(16), words=1, scale=0.0, out=P(16), ws=P(16), ws_bytes=1 << 30, err=None,
+            stream=None)
+
+
+def test_tree_refusals(L):
+    f = L.fp8attn_kv_tree_fwd
+    for change in (dict(rows=-1), dict(max_q=-1), dict(max_seq=-1), dict(total=-1), dict(heads=0),
+                   dict(kv=0), dict(heads=30), dict(width=0), dict(words=0), dict(scale=-1.0),
+                   dict(scale=float("nan")), dict(scale=float("inf")), dict(q=None),
+                   dict(out=None), dict(tables=None), dict(seq=None), dict(cu=None),
+                   dict(kc=None), dict(vc=None), dict(num=0), dict(stride=7)):
+        assert call(f, TREE, **change) == INVALID, change
+    for change in (dict(dim=64), dict(page=48), dict(rows=2049), dict(qt=4100), dict(qh=0),
+                   dict(q=P(8)), dict(out=P(8)), dict(mask=P(4)), dict(total=1 << 27),
+                   dict(chead=120), dict(ws=P(8))):
+        assert call(f, TREE, **change) == UNSUPPORTED, change
+    # bounds that allow 2^31 tiles and more
+    assert call(f, TREE, rows=2048, kv=32, width=1 << 20, stride=1 << 20,
+                max_seq=1 << 24) == UNSUPPORTED
+    need = L.fp8attn_kv_tree_workspace_bytes(64, 4, 4096, 32, 8)
+    assert need > 0
+    big = dict(rows=64, max_seq=4096, width=256, stride=256, total=256)
+    assert call(f, TREE, ws_bytes=need - 1, **big) == INVALID
+    assert call(f, TREE, ws=None, ws_bytes=need, **big) == INVALID
+    assert call(f, TREE, rows=0) == OK
+    assert call(f, TREE, total=0, q=None, out=None) == OK
+
+
+def test_tree_workspace(L):
+    f = L.fp8attn_kv_tree_workspace_bytes
+    for bad in ((0, 1, 1, 1, 1), (1, 0, 1, 1, 1), (1, 1, 0, 1, 1), (1, 1, 1, 3, 2), (1, 1, 1, 0, 1),
+                (2049, 1, 1, 1, 1)):
+        assert f(*bad) == 0
+    # grows with each bound, and stops at a CTA per SM
+    assert f(1, 1, 128, 8, 8) <= f(1, 1, 1 << 20, 8, 8) <= f(8, 1, 1 << 20, 8, 8)
+    assert f(8, 1, 1 << 20, 8, 8) <= f(8, 64, 1 << 20, 8, 8) <= 2 * 148 * 64 * (128 * 4 + 8)
+
+
+def test_keep_path_refusals(L):
+    base = dict(kc=P(16), vc=P(16), page_stride=16384, slot_stride=1024, chead=128, num=32,
+                page=16, elem=1, heads=8, dim=128, tables=P(16), stride=8, width=8, seq=P(16),
+                cu=P(16), rows=3, paths=P(16), path_stride=5, depth=5, keep=P(16), err=None,
+                stream=None)
+    f = L.fp8attn_kv_keep_path
+    for change in (dict(rows=-1), dict(depth=-1), dict(elem=4), dict(width=0), dict(tables=None),
+                   dict(seq=None), dict(cu=None), dict(paths=None), dict(keep=None),
+                   dict(path_stride=4), dict(stride=7), dict(kc=None), dict(num=0)):
+        assert call(f, base, **change) == INVALID, change
+    for change in (dict(dim=96), dict(page=7), dict(kc=P(8)), dict(slot_stride=1000)):
+        assert call(f, base, **change) == UNSUPPORTED, change
+    assert call(f, base, rows=0) == OK
+    assert call(f, base, depth=0) == OK
+
+
+def test_static_pointers_need_a_context(L):
+    assert L.fp8attn_static_quant_scale_ptr(None, 0) is None
+    assert L.fp8attn_static_descale_ptr(None, 0) is None
+    assert L.fp8attn_status_string(7) == b"page outside the cache, or too few free pages"
+
+
+def test_python_refuses_host_tensors():
+    import quantization_amax_reduce_b200 as qar
+    i = torch.zeros(2, dtype=torch.int32)
+    c = torch.zeros(2, 16, 1, 128, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="CUDA"):
+        qar.kv_assign_pages(i, i, torch.zeros(2, 4, dtype=torch.int32), i, i, i, 16, 0)
+    with pytest.raises(ValueError, match="CUDA"):
+        qar.kv_write(c, c, i, c, c)
+    with pytest.raises(ValueError, match="CUDA"):
+        qar.kv_tree_fwd(c, c, c, i, i, i, 1, 1)
+    with pytest.raises(ValueError, match="CUDA"):
+        qar.kv_keep_path(c, c, i, i, i, i, i)
+
+
+def test_reference_pool_restores_its_list():
+    """The definition's own property: taking pages and giving the same ones
+    back leaves the free list as it was (mixed growth and shrinkage between)."""
+    from tests.kv_reference import Pool
+    r = np.random.Generator(np.random.PCG64(4))
+    p = Pool(6, 20, 90, 16, r.permutation(90))
+    lens = r.integers(0, 100, 6)
+    assert p.assign(lens, lens, 600) is not None
+    before, owned = list(p.free), list(p.owned)
+    more = lens + r.integers(0, 60, 6)
+    assert p.assign(more, more - lens, 600) is not None
+    assert p.assign(lens, lens * 0, 0) is not None
+    assert p.free == before and p.owned == owned
+    assert p.assign(lens + 400, lens * 0, 0) is None and p.free == before
