@@ -17,11 +17,16 @@
 // holds one key and half of the rows: the row sum stays in its registers until
 // the unit ends, and the running maximum costs one vote per tile (see below).
 //
+//   warps 0-3, 4-7: two groups of 128 threads, each with half of the columns:
+//               softmax, P, epilogue
 //   warp 8      TMA producer: rings of K and V tiles, a box per page (page ids
 //               from the block table, one lane per page)
 //   warp 9      MMA issuer: S^T(t+1), then O^T += V^T P^T(t)
-//   warps 0-3, 4-7: two groups of 128 threads, each with half of the columns:
-//               Q into shared memory, V's E4M3 -> f16, softmax, P, epilogue
+//   warps 10-13 the next unit's Q into shared memory; V: E4M3 -> f16 into the
+//               buffer that the product reads, and the rows that must not touch
+//               it (past the sequence, non-finite)
+// One lane of a warp waits and arrives for it: 256 threads that each try the
+// same mbarrier cost some 250 cycles a time.
 //
 // E4M3 cache: K feeds kind::f8f6f4 as it lies.  A row of Q (bf16), scaled by a
 // power of two to [128, 256), is the sum of two E4M3 numbers to 2^-22 of its
@@ -59,28 +64,41 @@ namespace fp8attn {
 namespace {
 
 constexpr int kTile = 128;                 // keys of a tile
-constexpr int kSoftmaxThreads = 256;
-constexpr int kThreads = kSoftmaxThreads + 64;
-constexpr int kTmaWarp = 8, kMmaWarp = 9;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kPOffset = 8.0f;           // log2 of P at the reference
 constexpr float kRefLag = 7.0f;
 // A CTA's range is at least this many tiles: below it another CTA and the
 // join of its piece cost more than the tiles they save.
 constexpr int kMinTiles = 4;
+constexpr int kMaxCtas = 148;              // one per SM
 
+// One CTA per SM, whose stages hold as much in flight as they can: two CTAs of
+// half the stages each hid each other's unit switches, but read 3.7 TB/s where
+// one with deep rings reads 6.4 (16 columns, E4M3).
 template <int R, bool kFp8>
 struct Cfg {
-  static constexpr int kHalf = R / 2;                     // columns of a thread
+  static constexpr int kGroups = 2;
+  static constexpr int kCols = R / kGroups;               // columns of a softmax thread
+  static constexpr int kSoftmaxWarps = 4 * kGroups, kSoftmaxThreads = 128 * kGroups;
+  static constexpr int kTmaWarp = kSoftmaxWarps, kMmaWarp = kTmaWarp + 1;
+  static constexpr int kPrepWarp = kMmaWarp + 1, kPrepWarps = 4;
+  static constexpr int kThreads = 32 * (kPrepWarp + kPrepWarps);
   static constexpr int kN = kFp8 ? 2 * R : R;             // columns of S^T
   static constexpr int kKV = kFp8 ? 16384 : 32768;        // bytes of a K or V tile
-  static constexpr int kKStages = kFp8 ? 4 : 3;
-  static constexpr int kVStages = kFp8 ? 3 : 2;
-  static constexpr int kWide = kFp8 ? 2 * 32768 : 0;      // two f16 V tiles
+  static constexpr int kKStages = kFp8 ? (R == 16 ? 5 : 4) : 3;
+  static constexpr int kVStages = kFp8 ? (R == 64 ? 3 : 4) : (R == 64 ? 2 : 3);
+  static constexpr int kWide = kFp8 ? 2 : 0;              // f16 V tiles of 32 KB
+  // Rings of barriers: a waiter tests the parity of the phase it wants, so the
+  // phase after it on the same barrier must not end before the waiter passed.
+  static constexpr int kSRing = kKStages;
+  static constexpr int kPvRing = kFp8 ? kWide : kVStages;
+  static constexpr int kWideRing = kFp8 ? kWide : kVStages;
   static constexpr int kQ = R * 256;                      // hi and lo, or bf16
-  static constexpr int kP = kTile * 128;                  // 64 columns of 16 bits
-  static constexpr int kSmemData = kKStages * kKV + kVStages * kKV + kWide + kQ + kP;
+  static constexpr int kPitch = 2 * R;                    // bytes of a key's row of P
+  static constexpr int kP = kTile * kPitch;               // = R x 256: O^T is staged there
+  static constexpr int kSmemData = (kKStages + kVStages) * kKV + kWide * 32768 + kQ + kP;
   static constexpr uint32_t kO = 2 * kN;                  // TMEM column of O^T
+  static constexpr uint32_t kTmem = 512;
 };
 
 struct TreeArgs {
@@ -105,18 +123,41 @@ struct TreeArgs {
   int32_t* err;
 };
 
+// A CTA's tiles [t0, t1) of one unit.
+struct Segment {
+  int b, head, rt;       // request, KV head, row tile
+  int seq, q0, n;
+  int tiles, t0, t1;     // tiles of the unit; this CTA's (none: the end)
+};
+
+// What a unit's columns stand for.  Units u and u + 1 may be in use while unit
+// u + 2's slot is written.
+template <int R>
+struct Columns {
+  alignas(16) float2 scale[R];           // {S^T -> log2 units, kPOffset - ref}
+  int out_row[R];                        // row of `out`, -1 = none
+  int node[R];                           // -1 = none
+  Segment seg;
+};
+
+template <int R, bool kFp8>
 struct Control {
-  uint64_t k_full[4], k_empty[4], v_full[3], v_empty[3];
-  uint64_t s_full[2], s_free[2];
-  uint64_t q_full, p_full, pv_done, drain;
+  using C = Cfg<R, kFp8>;
+  // s_full: S^T of a tile is done, for the softmax, and its K stage is free;
+  // pv_done: O^T of a tile is done, and P, the widened V and a bf16 V stage
+  // are free.  One commit each: a commit costs the issuer as much as a product.
+  uint64_t k_full[C::kKStages], s_full[C::kSRing], v_full[C::kVStages], v_empty[C::kVStages];
+  uint64_t wide_full[C::kWideRing], pv_done[C::kPvRing];   // wide_full: V is as it is read
+  uint64_t q_full[2], p_full, drain;     // q_full: a unit's Q and columns are in place
   uint32_t tmem_base;
   int abort_flag;
-  int flagged[2];                        // a node's V of this unit holds Inf or NaN
-  int scan[kThreads / 32];
-  float factor[2][64];                   // S^T column -> log2 units
-  int out_row[2][64];                    // row of `out`, -1 = none
-  int node[2][64];
-  alignas(16) float red[2][32][4];       // [group][column][warp]
+  int flagged[4];                        // [u & 3] = u + 1: a node's V of unit u holds Inf or NaN
+  int warp_sums[16];
+  int chunk[C::kThreads + 1];            // tiles before a thread's requests
+  Columns<R> col[4];
+  float top[C::kGroups][4][C::kCols];    // [group][warp][column]
+  float sum[C::kGroups][4][C::kCols];
+  alignas(16) float bc[C::kSoftmaxWarps][2][C::kCols];   // a warp's values, lane -> all lanes
 };
 
 __device__ __forceinline__ void raise_error(int32_t* err, uint32_t bits) {
@@ -155,10 +196,11 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[N]) 
   else tmem_st32(taddr, r);
 }
 
-// Sums N columns (a power of two up to 32) over the warp's lanes: lane l gets
-// the sum of column l % N.
-template <int N>
-__device__ __forceinline__ float column_sum(float (&v)[N], int lane) {
+// Reduces N columns (a power of two up to 32) over the warp's lanes: lane l
+// gets column l % N.  N - 1 + log2(32 / N) shuffles instead of 5 N.
+template <int N, bool kMax>
+__device__ __forceinline__ float reduce_columns(float (&v)[N], int lane) {
+  auto join = [](float a, float b) { return kMax ? fmaxf(a, b) : a + b; };
 #pragma unroll
   for (int off = N / 2; off >= 1; off /= 2) {
     const bool up = (lane & off) != 0;
@@ -166,42 +208,79 @@ __device__ __forceinline__ float column_sum(float (&v)[N], int lane) {
     for (int i = 0; i < off; ++i) {
       const float send = up ? v[i] : v[i + off];
       const float mine = up ? v[i + off] : v[i];
-      v[i] = mine + __shfl_xor_sync(0xffffffffu, send, off);
+      v[i] = join(mine, __shfl_xor_sync(0xffffffffu, send, off));
     }
   }
 #pragma unroll
-  for (int off = N; off < 32; off *= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
+  for (int off = N; off < 32; off *= 2)
+    v[0] = join(v[0], __shfl_xor_sync(0xffffffffu, v[0], off));
   return v[0];
+}
+
+// Transposes a 32 x 32 bit matrix held one row per lane.
+__device__ __forceinline__ uint32_t transpose_bits(uint32_t x, int lane) {
+  uint32_t m = 0x0000FFFFu;
+#pragma unroll
+  for (int j = 16; j >= 1; j >>= 1, m ^= m << j) {
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, x, j);
+    x = (lane & j) ? (x & ~m) | ((y >> j) & m) : (x & m) | ((y & m) << j);
+  }
+  return x;
+}
+
+// Bits [j0, j0 + 32) of a mask row of `words` words; j0 > -32.
+__device__ __forceinline__ uint32_t mask_bits(const unsigned long long* row, int words, int j0) {
+  if (j0 < 0) return static_cast<uint32_t>(__ldg(row) << -j0);
+  const int w = j0 >> 6, sh = j0 & 63;
+  if (w >= words) return 0;
+  uint64_t v = __ldg(row + w) >> sh;
+  if (sh > 32 && w + 1 < words) v |= __ldg(row + w + 1) << (64 - sh);
+  return static_cast<uint32_t>(v);
+}
+
+__device__ __forceinline__ uint32_t low_bits(int n) {   // the n lowest bits, 0 <= n
+  return n >= 32 ? 0xffffffffu : (1u << n) - 1;
 }
 
 // ---------------------------------------------------------------------------
 // Work list: every role walks the same segments (a CTA's tiles of one unit).
 // ---------------------------------------------------------------------------
 
-__device__ __forceinline__ int row_tiles(int n, int group, int R) {
-  return (n * group + R - 1) / R;
+struct Request {
+  int seq, q0, n, tiles, row_tiles;
+  __device__ __forceinline__ int work(int kv_heads) const { return kv_heads * row_tiles * tiles; }
+};
+
+// A request's lengths; false if they are inconsistent (it then has no work).
+template <int R>
+__device__ __forceinline__ bool read_request(const TreeArgs& a, int b, Request& r) {
+  r.seq = a.seq[b];
+  r.q0 = a.cu[b];
+  const int q1 = a.cu[b + 1];
+  r.n = q1 - r.q0;
+  const bool ok = r.q0 >= 0 && q1 >= r.q0 && q1 <= a.total_q && r.n <= a.max_q && r.seq >= r.n &&
+                  r.seq <= a.max_seqlen &&
+                  r.seq <= static_cast<int64_t>(a.width) << a.page_log2 &&
+                  (!a.mask || r.n <= 64ll * a.mask_words);
+  r.tiles = ok ? (r.seq + kTile - 1) / kTile : 0;
+  r.row_tiles = ok ? (r.n * a.group + R - 1) / R : 0;
+  return ok;
 }
 
-// Tiles of the requests before each one into prefix[0..rows]; requests whose
-// lengths are inconsistent get none (and set `bad`).  All threads of the CTA.
-template <int kCtaThreads>
-__device__ void scan_requests(const TreeArgs& a, int R, int32_t* prefix, int* warp_sums,
-                              bool* bad) {
-  const int per = (a.rows + kCtaThreads - 1) / kCtaThreads;
+// chunk[i] = tiles of the requests before thread i's; chunk[kThreads] = all.
+// Returns whether this thread met an inconsistent request.
+template <int R, int kThreads>
+__device__ bool scan_requests(const TreeArgs& a, int* chunk, int* warp_sums) {
+  const int per = (a.rows + kThreads - 1) / kThreads;
   const int first = min(a.rows, static_cast<int>(threadIdx.x) * per);
   const int last = min(a.rows, first + per);
-  const int64_t held = static_cast<int64_t>(a.width) << a.page_log2;
-  auto tiles_of = [&](int b) {
-    const int seq = a.seq[b], q0 = a.cu[b], q1 = a.cu[b + 1], n = q1 - q0;
-    if (q0 < 0 || q1 < q0 || q1 > a.total_q || n > a.max_q || seq < n || seq > a.max_seqlen ||
-        seq > held || (a.mask && n > 64 * a.mask_words)) {
-      *bad = true;
-      return 0;
-    }
-    return a.kv_heads * row_tiles(n, a.group, R) * ((seq + kTile - 1) / kTile);
-  };
+  bool bad = false;
   int sum = 0;
-  for (int b = first; b < last; ++b) sum += tiles_of(b);
+  for (int b = first; b < last; ++b) {
+    Request r;
+    bad |= !read_request<R>(a, b, r);
+    sum += r.work(a.kv_heads);
+  }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int incl = sum;
 #pragma unroll
@@ -213,59 +292,70 @@ __device__ void scan_requests(const TreeArgs& a, int R, int32_t* prefix, int* wa
   __syncthreads();
   int at = incl - sum;
   for (int w = 0; w < warp; ++w) at += warp_sums[w];
-  for (int b = first; b < last; ++b) {
-    prefix[b] = at;
-    at += tiles_of(b);
-  }
-  if (threadIdx.x == kCtaThreads - 1) prefix[a.rows] = at;
-  __syncthreads();
+  chunk[threadIdx.x] = at;
+  if (threadIdx.x == kThreads - 1) chunk[kThreads] = at + sum;
+  return bad;   // (the caller syncs)
 }
 
-__device__ __forceinline__ int request_of(const int32_t* prefix, int rows, int w) {
-  int lo = 0, hi = rows - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (prefix[mid] <= w) lo = mid; else hi = mid - 1;
+// The request that a work item belongs to.
+template <int R, int kThreads>
+struct Finder {
+  Request r;
+  int b = -1, start = 0, stop = 0;   // request, its first item, end of its chunk
+  __device__ __forceinline__ void seek(const TreeArgs& a, const int* chunk, int w) {
+    if (b >= 0 && w < start + r.work(a.kv_heads)) return;
+    while (b >= 0 && b + 1 < stop) {   // a neighbour of the same chunk
+      start += r.work(a.kv_heads);
+      read_request<R>(a, ++b, r);
+      if (w < start + r.work(a.kv_heads)) return;
+    }
+    int lo = 0, hi = kThreads - 1;     // the last chunk that starts at or before w
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (chunk[mid] <= w) lo = mid; else hi = mid - 1;
+    }
+    const int per = (a.rows + kThreads - 1) / kThreads;
+    b = lo * per;
+    stop = min(a.rows, b + per);
+    start = chunk[lo];
+    read_request<R>(a, b, r);
+    while (w >= start + r.work(a.kv_heads)) {
+      start += r.work(a.kv_heads);
+      read_request<R>(a, ++b, r);
+    }
   }
-  return lo;
-}
+};
 
 // Tiles of a CTA's range.
 __device__ __forceinline__ int tiles_per_cta(int total, int ctas) {
   return max(kMinTiles, (total + ctas - 1) / ctas);
 }
 
-struct Segment {
-  int b, head, rt;       // request, KV head, row tile
-  int seq, q0, n;
-  int tiles, t0, t1;     // tiles of the unit; this CTA's [t0, t1)
-};
-
+template <int R, int kThreads>
 struct Walker {
-  int w, end, b;
-  __device__ __forceinline__ void init(const TreeArgs& a, const int32_t* prefix, int ctas) {
-    const int total = prefix[a.rows];
+  Finder<R, kThreads> find;
+  int w, end;
+  __device__ __forceinline__ void init(const int* chunk, int ctas) {
+    const int total = chunk[kThreads];
     const int per = tiles_per_cta(total, ctas);
     const int64_t from = static_cast<int64_t>(blockIdx.x) * per;
     w = static_cast<int>(min(from, static_cast<int64_t>(total)));
     end = static_cast<int>(min(from + per, static_cast<int64_t>(total)));
-    b = w < end ? request_of(prefix, a.rows, w) : 0;
   }
-  __device__ __forceinline__ bool next(const TreeArgs& a, int R, const int32_t* prefix,
-                                       Segment& s) {
+  __device__ __forceinline__ bool next(const TreeArgs& a, const int* chunk, Segment& s) {
     if (w >= end) return false;
-    while (prefix[b + 1] <= w) ++b;
-    s.b = b;
-    s.seq = a.seq[b];
-    s.q0 = a.cu[b];
-    s.n = a.cu[b + 1] - s.q0;
-    s.tiles = (s.seq + kTile - 1) / kTile;
-    const int rts = row_tiles(s.n, a.group, R);
-    const int local = w - prefix[b];
-    const int unit = local / s.tiles;
-    s.head = unit / rts;
-    s.rt = unit - s.head * rts;
-    s.t0 = local - unit * s.tiles;
+    find.seek(a, chunk, w);
+    const Request& r = find.r;
+    s.b = find.b;
+    s.seq = r.seq;
+    s.q0 = r.q0;
+    s.n = r.n;
+    s.tiles = r.tiles;
+    const int local = w - find.start;
+    const int unit = local / r.tiles;
+    s.head = unit / r.row_tiles;
+    s.rt = unit - s.head * r.row_tiles;
+    s.t0 = local - unit * r.tiles;
     s.t1 = min(s.tiles, s.t0 + (end - w));
     w += s.t1 - s.t0;
     return true;
@@ -274,14 +364,8 @@ struct Walker {
 
 // ---------------------------------------------------------------------------
 
-template <bool kFp8>
-__device__ __forceinline__ float v_value(const uint8_t* p, int64_t i) {
-  if (kFp8) return __uint_as_float((p[i] & 0x7Fu) == 0x7Fu ? 0x7FC00000u : 0u);   // NaN or not
-  return __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[i]) << 16);
-}
-
 template <int R, bool kFp8>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<R, kFp8>::kThreads, 1)
 kv_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                const TreeArgs a) {
   using C = Cfg<R, kFp8>;
@@ -291,71 +375,86 @@ kv_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   uint8_t* sk = smem;
   uint8_t* sv = sk + C::kKStages * C::kKV;
   uint8_t* swide = sv + C::kVStages * C::kKV;
-  uint8_t* sq = swide + C::kWide;
+  uint8_t* sq = swide + C::kWide * 32768;
   uint8_t* sp = sq + C::kQ;
-  Control& ctl = *reinterpret_cast<Control*>(sp + C::kP);
-  int32_t* prefix = reinterpret_cast<int32_t*>(&ctl + 1);
+  Control<R, kFp8>& ctl = *reinterpret_cast<Control<R, kFp8>*>(sp + C::kP);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // the join starts as SMs free up; it waits for this grid before it reads
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&ctl.k_full[i], 1);
-      mbar_init(&ctl.k_empty[i], 1);
-    }
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < C::kKStages; ++i) mbar_init(&ctl.k_full[i], 1);
+    for (int i = 0; i < C::kSRing; ++i) mbar_init(&ctl.s_full[i], 1);
+    for (int i = 0; i < C::kVStages; ++i) {
       mbar_init(&ctl.v_full[i], 1);
-      mbar_init(&ctl.v_empty[i], kFp8 ? kSoftmaxThreads / 32 : 1);
+      mbar_init(&ctl.v_empty[i], C::kPrepWarps);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl.s_full[i], 1);
-      mbar_init(&ctl.s_free[i], kSoftmaxThreads);
-    }
-    mbar_init(&ctl.q_full, kSoftmaxThreads);
-    mbar_init(&ctl.p_full, kSoftmaxThreads);
-    mbar_init(&ctl.pv_done, 1);
+    for (int i = 0; i < C::kWideRing; ++i) mbar_init(&ctl.wide_full[i], C::kPrepWarps);
+    for (int i = 0; i < C::kPvRing; ++i) mbar_init(&ctl.pv_done[i], 1);
+    for (int i = 0; i < 4; ++i) ctl.flagged[i] = 0;
+    mbar_init(&ctl.q_full[0], C::kPrepWarps);
+    mbar_init(&ctl.q_full[1], C::kPrepWarps);
+    mbar_init(&ctl.p_full, C::kSoftmaxWarps);
     mbar_init(&ctl.drain, 1);
     ctl.abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kTmaWarp && lane == 0) {
+  if (warp == C::kTmaWarp && lane == 0) {
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
-  if (warp == kMmaWarp) {
-    tmem_alloc(&ctl.tmem_base, 512);
+  if (warp == C::kMmaWarp) {
+    tmem_alloc(&ctl.tmem_base, C::kTmem);
     tmem_relinquish();
   }
-  bool bad = false;
-  scan_requests<kThreads>(a, R, prefix, ctl.scan, &bad);
+  const bool bad = scan_requests<R, C::kThreads>(a, ctl.chunk, ctl.warp_sums);
   if (bad && blockIdx.x == 0) raise_error(a.err, kErrSeqlens);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl.tmem_base;
   const volatile int* abort_flag = &ctl.abort_flag;
-  Walker walk;
-  walk.init(a, prefix, gridDim.x);
-  Segment seg;
+  // One lane waits and arrives for its warp.  A wait that gives up sets the
+  // abort flag, which ends all other waits at once; the roles then run on
+  // without data (so that every barrier is met) and write no output.
+  auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
+    if (lane == 0 && !mbar_wait(bar, parity, abort_flag)) {
+      if (!*abort_flag) raise_error(a.err, kErrTimeout);
+      ctl.abort_flag = 1;
+    }
+    __syncwarp();
+  };
+  auto arrive_warp = [&](uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
+  auto wait_pv = [&](int g) { wait_warp(&ctl.pv_done[g % C::kPvRing], (g / C::kPvRing) & 1); };
+  // the preparing warps hand out the units, with their Q; a copy ends the loop
+  auto unit_at = [&](int unit, Segment& s) {
+    wait_warp(&ctl.q_full[unit & 1], (unit >> 1) & 1);
+    s = ctl.col[unit & 3].seg;
+    return s.t0 < s.t1 && !*abort_flag;
+  };
 
-  if (warp == kTmaWarp) {
+  if (warp == C::kTmaWarp) {
     // ------------------------------------------------------------ producer
     const int page = 1 << a.page_log2;
     const int box = min(page, kTile);
-    const int page_rows_log2 = min(a.page_log2, 7);
+    const int box_log2 = min(a.page_log2, 7);
+    Walker<R, C::kThreads> walk;
+    walk.init(ctl.chunk, gridDim.x);
+    Segment seg;
     int g = 0;
-    bool ok = true;
-    while (ok && walk.next(a, R, prefix, seg)) {
+    while (!*abort_flag && walk.next(a, ctl.chunk, seg)) {
       const int32_t* table = a.tables + seg.b * a.table_stride;
       // the page of this lane's box of tile t, looked up a tile ahead
       auto look_up = [&](int t) {
-        const int key = t * kTile + (lane << page_rows_log2);
-        if (lane >= kTile >> page_rows_log2 || key >= seg.seq) return -2;
+        const int key = t * kTile + (lane << box_log2);
+        if (lane >= kTile >> box_log2 || key >= seg.seq) return -2;
         return __ldg(table + (key >> a.page_log2));
       };
       int next_id = look_up(seg.t0);
-      for (int t = seg.t0; t < seg.t1 && ok; ++t, ++g) {
+      for (int t = seg.t0; t < seg.t1; ++t, ++g) {
         const int id = next_id;
         if (t + 1 < seg.t1) next_id = look_up(t + 1);
         const bool load = id != -2;
@@ -363,9 +462,10 @@ kv_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, load)) * box * (kFp8 ? 128 : 256);
         const int row = a.page_log2 > 7 ? (t * kTile) & (page - 1) : 0;
         const int ks = g % C::kKStages, vs = g % C::kVStages;
-        // a page id outside the cache is outside the tensor map: zeros arrive
-        if (g >= C::kKStages) ok = mbar_wait(&ctl.k_empty[ks], (g / C::kKStages - 1) & 1, abort_flag);
-        if (!ok) break;
+        // a page id outside the cache is outside the tensor map: zeros arrive;
+        // after an abort the copies go on, into stages that nobody reads
+        const int freed = g - C::kKStages;      // its S^T frees the stage
+        if (freed >= 0) wait_warp(&ctl.s_full[freed % C::kSRing], (freed / C::kSRing) & 1);
         if (lane == 0) mbar_expect_tx(&ctl.k_full[ks], bytes);
         __syncwarp();
         if (load) {
@@ -373,10 +473,9 @@ kv_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           tma_load_4d(dst, &tm_k, &ctl.k_full[ks], 0, seg.head, row, id);
           if (!kFp8) tma_load_4d(dst + 16384, &tm_k, &ctl.k_full[ks], 64, seg.head, row, id);
         }
-        if (g >= C::kVStages) ok = mbar_wait(&ctl.v_empty[vs], (g / C::kVStages - 1) & 1, abort_flag);
-        if (!ok) {
-          ++g;   // this tile's K is in flight
-          break;
+        if (g >= C::kVStages) {
+          wait_warp(&ctl.v_empty[vs], (g / C::kVStages - 1) & 1);
+          if (!kFp8) wait_pv(g - C::kVStages);
         }
         if (lane == 0) mbar_expect_tx(&ctl.v_full[vs], bytes);
         __syncwarp();
@@ -385,133 +484,125 @@ kv_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           tma_load_4d(dst, &tm_v, &ctl.v_full[vs], 0, seg.head, row, id);
           if (!kFp8) tma_load_4d(dst + 16384, &tm_v, &ctl.v_full[vs], 64, seg.head, row, id);
         }
+        __syncwarp();
       }
     }
-    if (!ok && lane == 0) {
-      ctl.abort_flag = 1;
-      raise_error(a.err, kErrTimeout);
+    // no copy may still be landing when the CTA leaves
+    if (lane == 0) {
+      for (int i = max(0, g - C::kKStages); i < g; ++i)
+        mbar_wait(&ctl.k_full[i % C::kKStages], (i / C::kKStages) & 1, nullptr);
+      for (int i = max(0, g - C::kVStages); i < g; ++i)
+        mbar_wait(&ctl.v_full[i % C::kVStages], (i / C::kVStages) & 1, nullptr);
     }
     __syncwarp();
-    // no copy may still be landing when the CTA leaves (a wait on a V tile
-    // that was not issued ends at its limit, after an abort only)
-    for (int i = max(0, g - C::kKStages); i < g; ++i)
-      mbar_wait(&ctl.k_full[i % C::kKStages], (i / C::kKStages) & 1, nullptr);
-    for (int i = max(0, g - C::kVStages); i < g; ++i)
-      mbar_wait(&ctl.v_full[i % C::kVStages], (i / C::kVStages) & 1, nullptr);
-  } else if (warp == kMmaWarp) {
+  } else if (warp == C::kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
+    // (the whole warp walks, one elected lane issues: descriptors then stay in
+    // uniform registers; a lone thread took twice the cycles per product)
     const uint32_t id_s = kFp8 ? make_idesc(0, 0, C::kN, 0) : make_idesc(1, 1, C::kN, 0);
     const uint32_t id_pv = make_idesc(kFp8 ? 0 : 1, kFp8 ? 0 : 1, R, 1) | kIdescAMnMajor;
     const uint64_t dk0 = make_sdesc_sw128(smem_u32(sk), 16, 1024);
     const uint64_t dq0 = make_sdesc_sw128(smem_u32(sq), 16, 1024);
     const uint64_t dv0 = make_sdesc_sw128(smem_u32(kFp8 ? swide : sv), 16384, 1024);
-    const uint64_t dp0 = make_sdesc_sw128(smem_u32(sp), 16384, 1024);
-    auto issue_s = [&](int g) {
-      const uint64_t dk = dk0 + static_cast<uint64_t>((g % C::kKStages) * (C::kKV >> 4));
-      const uint32_t d = tmem + (g & 1) * C::kN;
-      if (elect_one()) {
-        if constexpr (kFp8) {
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) mma_f8_ss(d, dk + 2 * kk, dq0 + 2 * kk, id_s, kk > 0);
-        } else {
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_bf16_ss(d, dk + (kk >> 2) * 1024 + 2 * (kk & 3),
-                        dq0 + (kk >> 2) * (R * 128 >> 4) + 2 * (kk & 3), id_s, kk > 0);
-        }
-        mma_commit(&ctl.s_full[g & 1]);
-        mma_commit(&ctl.k_empty[g % C::kKStages]);
-      }
-      __syncwarp();
-    };
-    auto issue_pv = [&](int g, bool first) {
-      const uint64_t dv =
-          dv0 + static_cast<uint64_t>(kFp8 ? (g & 1) * 2048 : (g % C::kVStages) * 2048);
-      if (elect_one()) {
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_bf16_ss(tmem + C::kO, dv + 128 * kk, dp0 + 128 * kk, id_pv, kk > 0 || !first);
-        mma_commit(&ctl.pv_done);
-        if (!kFp8) mma_commit(&ctl.v_empty[g % C::kVStages]);
-      }
-      __syncwarp();
-    };
-    bool ok = true;
-    int g = 0, units = 0;      // tiles whose S is issued; segments begun
-    bool pending = false, pending_first = false;
+    const uint64_t dp0 = make_sdesc(smem_u32(sp), 16384, 8 * C::kPitch,
+                                    R == 16 ? kSwizzle32 : R == 32 ? kSwizzle64 : kSwizzle128);
+    Segment seg;
+    int g = 0;                 // tiles whose S is issued
+    int tails = 0;             // bf16: tiles whose V went through the value warps
+    bool pending = false, pending_first = false, pending_tail = false;
     auto finish = [&]() {      // O^T += V^T P^T of tile g - 1
       if (!pending) return;
       const int p = g - 1;
-      ok = ok && (kFp8 || mbar_wait(&ctl.v_full[p % C::kVStages], (p / C::kVStages) & 1, abort_flag)) &&
-           mbar_wait(&ctl.p_full, p & 1, abort_flag);
-      if (ok) {
-        tc_fence_after();
-        issue_pv(p, pending_first);
-      }
       pending = false;
+      if (kFp8 || pending_tail) {
+        const int i = kFp8 ? p : tails++;
+        wait_warp(&ctl.wide_full[i % C::kWideRing], (i / C::kWideRing) & 1);
+      } else {
+        wait_warp(&ctl.v_full[p % C::kVStages], (p / C::kVStages) & 1);
+      }
+      wait_warp(&ctl.p_full, p & 1);
+      tc_fence_after();
+      const uint64_t dv =
+          dv0 + static_cast<uint64_t>((p % (kFp8 ? C::kWide : C::kVStages)) * (32768 >> 4));
+      const uint32_t acc0 = pending_first ? 0u : 1u;
+      uint64_t ad[8], bd[8];
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        ad[kk] = dv + 128 * kk;          // both MN-major: 16 keys' rows per MMA
+        bd[kk] = dp0 + C::kPitch * kk;
+      }
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_bf16_ss(tmem + C::kO, ad[kk], bd[kk], id_pv, kk > 0 ? 1u : acc0);
+        mma_commit(&ctl.pv_done[p % C::kPvRing]);
+      }
+      __syncwarp();
     };
-    while (ok && walk.next(a, R, prefix, seg)) {
-      // a new unit's Q arrives only after the last unit's epilogue
+    for (int unit = 0;; ++unit) {
       finish();
-      ok = ok && mbar_wait(&ctl.q_full, units & 1, abort_flag);
-      ++units;
-      for (int t = seg.t0; t < seg.t1 && ok; ++t) {
+      if (!unit_at(unit, seg)) break;
+      for (int t = seg.t0; t < seg.t1; ++t) {
         const int ks = g % C::kKStages;
-        ok = mbar_wait(&ctl.k_full[ks], (g / C::kKStages) & 1, abort_flag) &&
-             (g < 2 || mbar_wait(&ctl.s_free[g & 1], ((g >> 1) - 1) & 1, abort_flag));
-        if (!ok) break;
+        // (the softmax has read S^T of tile g - 2: its P was waited for)
+        wait_warp(&ctl.k_full[ks], (g / C::kKStages) & 1);
         tc_fence_after();
-        issue_s(g);
+        const uint64_t dk = dk0 + static_cast<uint64_t>(ks * (C::kKV >> 4));
+        const uint32_t d = tmem + (g & 1) * C::kN;
+        constexpr int kSteps = kFp8 ? 4 : 8;
+        uint64_t ad[kSteps], bd[kSteps];
+#pragma unroll
+        for (int kk = 0; kk < kSteps; ++kk) {
+          ad[kk] = dk + (kk >> 2) * 1024 + 2 * (kk & 3);
+          bd[kk] = dq0 + (kk >> 2) * (R * 128 >> 4) + 2 * (kk & 3);
+        }
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < kSteps; ++kk) {
+            if (kFp8) mma_f8_ss(d, ad[kk], bd[kk], id_s, kk > 0);
+            else mma_bf16_ss(d, ad[kk], bd[kk], id_s, kk > 0);
+          }
+          mma_commit(&ctl.s_full[g % C::kSRing]);
+        }
+        __syncwarp();
         finish();
         ++g;
         pending = true;
         pending_first = t == seg.t0;
+        pending_tail = t * kTile + kTile > seg.seq - seg.n;
       }
     }
-    finish();
-    if (!ok && lane == 0) {
-      ctl.abort_flag = 1;
-      raise_error(a.err, kErrTimeout);
-    }
-    __syncwarp();
     // drain: every MMA issued has completed before TMEM is freed
     if (elect_one()) mma_commit(&ctl.drain);
     __syncwarp();
-    mbar_wait(&ctl.drain, 0, nullptr);
-  } else {
-    // ------------------------------------------------------------ softmax
-    // After a failed wait (abort) the threads run on without data, so that
-    // every named barrier is met, and write nothing.
-    const int wg = warp >> 2, wq = warp & 3;
-    const int tid = threadIdx.x;
-    const int key = 32 * wq + lane;                 // lane of TMEM: key, or channel
-    const int bar_wg = 1 + wg;
-    const uint32_t lane_off = static_cast<uint32_t>(32 * wq) << 16;
-    const uint32_t t_s = tmem + lane_off + wg * C::kHalf;
-    const uint32_t t_o = tmem + lane_off + C::kO + wg * C::kHalf;
-    const int col0 = wg * C::kHalf;
-    uint8_t* prow = sp + (key >> 3) * 1024 + (key & 7) * 128;
+    if (lane == 0) mbar_wait(&ctl.drain, 0, nullptr);
+    __syncwarp();
+  } else if (warp >= C::kPrepWarp) {
+    // ------------------------------------------------------------ Q and V
+    const int tid = threadIdx.x - C::kPrepWarp * 32;
     const float unit_factor =
         a.softmax_scale * kLog2e * (kFp8 ? __ldg(a.descale + 1) : 1.0f);
-    const float ds_v = kFp8 ? __ldg(a.descale + 2) : 1.0f;
-    bool ok = true;
-    int g = 0, units = 0;
-    while (walk.next(a, R, prefix, seg)) {
-      const int par = units & 1;
-      const int ctx = seg.seq - seg.n;
-      // ---- Q rows of the unit, and what each column stands for
-      if (tid == 0) ctl.flagged[par] = 0;
+    // Q: a half warp per row, 8 channels a lane; loaded a unit ahead
+    constexpr int kLoads = R / 8;
+    uint4 xq[kLoads];
+    auto load_q = [&](const Segment& s) {
 #pragma unroll
-      for (int it = 0; it < R * 16 / kSoftmaxThreads; ++it) {
-        const int r = it * 16 + (tid >> 4), c = tid & 15;   // row, 8-channel piece
-        const int row = seg.rt * R + r;
+      for (int it = 0; it < kLoads; ++it) {
+        const int row = s.rt * R + it * 8 + (tid >> 4);
         const int node = row / a.group, gq = row - node * a.group;
-        const bool live = node < seg.n;
-        const int head = seg.head * a.group + gq;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (live)
-          x = __ldg(reinterpret_cast<const uint4*>(a.q + (seg.q0 + node) * a.q_tok_stride +
-                                                   head * a.q_head_stride + c * 8));
+        xq[it] = make_uint4(0, 0, 0, 0);
+        if (node < s.n)
+          xq[it] = __ldg(reinterpret_cast<const uint4*>(
+              a.q + (s.q0 + node) * a.q_tok_stride +
+              (s.head * a.group + gq) * a.q_head_stride + (tid & 15) * 8));
+      }
+    };
+    auto store_q = [&](const Segment& s, Columns<R>& col) {
+      const int c = tid & 15;
+#pragma unroll
+      for (int it = 0; it < kLoads; ++it) {
+        const int r = it * 8 + (tid >> 4);
+        const uint4 x = xq[it];
         float factor = unit_factor;
         if constexpr (kFp8) {
           const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -538,285 +629,375 @@ kv_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             hi[i >> 1] |= (whole ? h : 0x7F7Fu) << (16 * (i & 1));
             lo[i >> 1] |= (whole ? l : 0x7F7Fu) << (16 * (i & 1));
           }
-          auto at = [&](int rr) {
-            return sq + (rr >> 3) * 1024 + (rr & 7) * 128 + (((c >> 1) ^ (rr & 7)) << 4) +
-                   (c & 1) * 8;
-          };
-          *reinterpret_cast<uint2*>(at(r)) = make_uint2(hi[0], hi[1]);
-          *reinterpret_cast<uint2*>(at(R + r)) = make_uint2(lo[0], lo[1]);
+          uint8_t* to = sq + (r >> 3) * 1024 + (r & 7) * 128 + (((c >> 1) ^ (r & 7)) << 4) +
+                        (c & 1) * 8;
+          *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(to + R * 128) = make_uint2(lo[0], lo[1]);   // row R + r
         } else {
           *reinterpret_cast<uint4*>(sq + (c >> 3) * (R * 128) + (r >> 3) * 1024 + (r & 7) * 128 +
                                     (((c & 7) ^ (r & 7)) << 4)) = x;
         }
-        if (c == 0) {
-          ctl.factor[par][r] = factor;
-          ctl.node[par][r] = live ? node : -1;
-          ctl.out_row[par][r] = live ? (seg.q0 + node) * (a.kv_heads * a.group) + head : -1;
-        }
+        if (c == 0) col.scale[r] = make_float2(factor, 0.0f);
       }
+      if (tid < R) {
+        const int row = s.rt * R + tid;
+        const int node = row / a.group, gq = row - node * a.group;
+        const bool live = node < s.n;
+        col.node[tid] = live ? node : -1;
+        col.out_row[tid] =
+            live ? (s.q0 + node) * (a.kv_heads * a.group) + s.head * a.group + gq : -1;
+      }
+      if (tid == 0) col.seg = s;
       fence_proxy_async();
-      mbar_arrive(&ctl.q_full);
-      group_sync(3, kSoftmaxThreads);
+    };
+    Walker<R, C::kThreads> walk;
+    walk.init(ctl.chunk, gridDim.x);
+    Segment seg, next;
+    bool more = walk.next(a, ctl.chunk, next);
+    if (more) load_q(next);
+    int g = 0, units = 0, tails = 0;
+    for (;;) {
+      seg = next;
+      // Q's place is free when the last unit's last S^T is done
+      if (g > 0) wait_warp(&ctl.s_full[(g - 1) % C::kSRing], ((g - 1) / C::kSRing) & 1);
+      if (more) store_q(seg, ctl.col[units & 3]);
+      else if (tid == 0) ctl.col[units & 3].seg.t0 = ctl.col[units & 3].seg.t1 = 0;
+      arrive_warp(&ctl.q_full[units & 1]);
+      if (!more) break;
+      more = walk.next(a, ctl.chunk, next);
+      if (more) load_q(next);
+      // V.  In tiles that hold nodes, rows past the sequence become zeros, and
+      // so do the non-finite elements of nodes, which a query that does not
+      // see the node must not meet as 0 x Inf: the epilogue adds them.
+      const int ctx = seg.seq - seg.n;
       ++units;
-
-      float off[C::kHalf];      // kPOffset - ref, 0 while unset
-      float sum[C::kHalf];
-      uint32_t unset = C::kHalf == 32 ? 0xffffffffu : (1u << C::kHalf) - 1;
-#pragma unroll
-      for (int c = 0; c < C::kHalf; ++c) off[c] = sum[c] = 0.0f;
-
-      auto sees = [&](int c, int j) {   // does column c see node j >= 0?
-        const int node = ctl.node[par][col0 + c];
-        if (j >= seg.n || node < 0) return false;
-        if (!a.mask) return j <= node;
-        const unsigned long long word =
-            __ldg(a.mask + static_cast<int64_t>(seg.q0 + node) * a.mask_words + (j >> 6));
-        return ((word >> (j & 63)) & 1) != 0;
-      };
-
       for (int t = seg.t0; t < seg.t1; ++t, ++g) {
-        const int j = t * kTile + key - ctx;            // node of this thread's key, < 0: context
-        const bool tail = t * kTile + kTile > ctx;      // the tile holds nodes
+        const bool tail = t * kTile + kTile > ctx;
         const int vs = g % C::kVStages;
-        // ---- V: E4M3 -> f16 (buffer g & 1 is free: its last reader, the
-        // product of tile g - 2, was waited for before P of tile g - 1 was
-        // written).  In the tail, rows past the sequence become zeros, and so
-        // do the non-finite elements of nodes, which a row that does not see
-        // the node must not meet as 0 x Inf: the epilogue adds them.
+        uint8_t* src = sv + vs * C::kKV;
+        bool wild = false;
+        wait_warp(&ctl.v_full[vs], (g / C::kVStages) & 1);
+        if (!kFp8 && !tail) {   // nothing to do; the stage's next phase may begin
+          arrive_warp(&ctl.v_empty[vs]);
+          continue;
+        }
         if constexpr (kFp8) {
-          ok = ok && mbar_wait(&ctl.v_full[vs], (g / C::kVStages) & 1, abort_flag);
-          const uint8_t* src = sv + vs * C::kKV;
-          uint4 x[4];
+          constexpr int kRows = C::kPrepWarps * 4;   // rows of one pass of the threads
+          uint8_t* wide = swide + (g % C::kWide) * 32768;
+          // a thread's pieces of 16 channels: c = tid & 7 of rows kRows i + tid / 8.
+          // They become pieces 2 (c & 3) and + 1 of half c >> 2; the halves
+          // start with different ones (no bank conflicts).
+          const int row = tid >> 3, c = tid & 7, odd = c >> 2;
+          uint8_t* to = wide + odd * 16384 + row * 128;
+          const int p0 = ((2 * (c & 3) + odd) ^ (row & 7)) << 4;
+          const int p1 = ((2 * (c & 3) + (odd ^ 1)) ^ (row & 7)) << 4;
+#pragma unroll 1
+          for (int i0 = 0; i0 < kTile / kRows; i0 += 8) {
+            uint4 x[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            x[i] = *reinterpret_cast<const uint4*>(src + (i * 256 + (tid ^ ((tid >> 3) & 7))) * 16);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl.v_empty[vs]);
-          uint8_t* dst = swide + (g & 1) * 32768;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = i * 32 + (tid >> 3), c = tid & 7;   // key, 16-channel piece
+            for (int i = 0; i < 8; ++i)
+              x[i] = *reinterpret_cast<const uint4*>(
+                  src + ((i0 + i) * kRows * 8 + (tid ^ ((tid >> 3) & 7))) * 16);
+            if (i0 + 8 == kTile / kRows) arrive_warp(&ctl.v_empty[vs]);
             if (tail) {
-              const int pos = t * kTile + row;
-              if (pos >= seg.seq) {
-                x[i] = make_uint4(0, 0, 0, 0);
-              } else if (pos >= ctx) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int pos = t * kTile + (i0 + i) * kRows + row;
                 uint32_t* w = &x[i].x;
                 uint32_t nan = 0;
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                  const uint32_t m = __vcmpeq4(w[u] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                  const uint32_t m = pos >= seg.seq ? 0xffffffffu
+                                     : pos >= ctx   ? __vcmpeq4(w[u] & 0x7F7F7F7Fu, 0x7F7F7F7Fu)
+                                                    : 0u;
                   w[u] &= ~m;
                   nan |= m;
                 }
-                if (nan) ctl.flagged[par] = 1;
+                wild |= nan != 0 && pos < seg.seq;
               }
             }
-            uint32_t f[8];
+            if (i0 == 0 && g >= C::kWide) wait_pv(g - C::kWide);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const uint32_t w = (&x[i].x)[u];
-              f[2 * u] = cvt_f16x2_from_e4m3x2(w & 0xFFFFu);
-              f[2 * u + 1] = cvt_f16x2_from_e4m3x2(w >> 16);
+            for (int i = 0; i < 8; ++i) {
+              uint32_t f[8];
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const uint32_t w = (&x[i].x)[u];
+                f[2 * u] = cvt_f16x2_from_e4m3x2(w & 0xFFFFu);
+                f[2 * u + 1] = cvt_f16x2_from_e4m3x2(w >> 16);
+              }
+              const uint4 lo = make_uint4(f[0], f[1], f[2], f[3]);
+              const uint4 hi = make_uint4(f[4], f[5], f[6], f[7]);
+              uint8_t* d = to + (i0 + i) * kRows * 128;
+              *reinterpret_cast<uint4*>(d + p0) = odd ? hi : lo;
+              *reinterpret_cast<uint4*>(d + p1) = odd ? lo : hi;
             }
-            // channels 16 c .. 16 c + 15: pieces 2 (c & 3), + 1 of half c >> 2;
-            // the halves start with different ones (no bank conflicts)
-            uint8_t* to = dst + (c >> 2) * 16384 + (row >> 3) * 1024 + (row & 7) * 128;
-            const int odd = c >> 2;
-            const int p0 = 2 * (c & 3) + odd, p1 = 2 * (c & 3) + (odd ^ 1);
-            const uint4 lo = make_uint4(f[0], f[1], f[2], f[3]);
-            const uint4 hi = make_uint4(f[4], f[5], f[6], f[7]);
-            *reinterpret_cast<uint4*>(to + ((p0 ^ (row & 7)) << 4)) = odd ? hi : lo;
-            *reinterpret_cast<uint4*>(to + ((p1 ^ (row & 7)) << 4)) = odd ? lo : hi;
           }
-        } else if (tail) {
-          ok = ok && mbar_wait(&ctl.v_full[vs], (g / C::kVStages) & 1, abort_flag);
-          uint8_t* src = sv + vs * C::kKV;
-          for (int i = tid; i < C::kKV / 16; i += kSoftmaxThreads) {
+        } else {
+          for (int i = tid; i < C::kKV / 16; i += 32 * C::kPrepWarps) {
             const int pos = t * kTile + ((i >> 3) & 127);
             if (pos < ctx) continue;
             uint4* p = reinterpret_cast<uint4*>(src + i * 16);
             uint4 x = pos < seg.seq ? *p : make_uint4(0, 0, 0, 0);
             uint32_t* w = &x.x;
-            uint32_t wild = pos < seg.seq ? 0u : 1u;
+            uint32_t m_any = 0;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
               const uint32_t m = __vcmpeq2(w[u] & 0x7F807F80u, 0x7F807F80u);
               w[u] &= ~m;
-              wild |= m;
+              m_any |= m;
             }
-            if (wild) {
-              *p = x;
-              if (pos < seg.seq) ctl.flagged[par] = 1;
-            }
+            if (m_any || pos >= seg.seq) *p = x;
+            wild |= m_any != 0;
           }
+        }
+        fence_proxy_async();
+        if (wild) *const_cast<volatile int*>(&ctl.flagged[units & 3]) = units;
+        const int i = kFp8 ? g : tails++;
+        arrive_warp(&ctl.wide_full[i % C::kWideRing]);
+        if (!kFp8) arrive_warp(&ctl.v_empty[vs]);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    constexpr int kCols = C::kCols, kPart = kCols < 16 ? kCols : 16;
+    const int wg = warp >> 2, wq = warp & 3;
+    const int key = 32 * wq + lane;                 // lane of TMEM: key, or channel
+    const int bar_wg = 1 + wg;
+    const uint32_t lane_off = static_cast<uint32_t>(32 * wq) << 16;
+    const uint32_t t_s = tmem + lane_off + wg * kCols;
+    const uint32_t t_o = tmem + lane_off + C::kO + wg * kCols;
+    const int col0 = wg * kCols;
+    const int c_mine = lane & (kCols - 1);          // where a lane stands for a column
+    constexpr uint32_t kAll = kCols == 32 ? 0xffffffffu : (1u << kCols) - 1;
+    // this key's row of P; 16-byte pieces are swizzled by address bits 7 and up
+    uint8_t* prow = sp + key * C::kPitch;
+    const int pswz = R == 64 ? key & 7 : R == 32 ? (key >> 1) & 3 : (key >> 2) & 1;
+    const float ds_v = kFp8 ? __ldg(a.descale + 2) : 1.0f;
+    Segment seg;
+    int g = 0;
+    for (int unit = 0; unit_at(unit, seg); ++unit) {
+      Columns<R>& col = ctl.col[unit & 3];
+      const int ctx = seg.seq - seg.n;
+      float sum[kCols];
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) sum[c] = 0.0f;
+      const int my_node = col.node[col0 + c_mine];
+      const unsigned long long* my_mask =
+          a.mask + static_cast<int64_t>(seg.q0 + max(my_node, 0)) * a.mask_words;
+      float my_off = 0.0f;      // kPOffset - ref, 0 while unset
+      // live columns that have met no visible key yet
+      uint32_t unset = __ballot_sync(0xffffffffu, my_node >= 0) & kAll;
+
+      for (int t = seg.t0; t < seg.t1; ++t, ++g) {
+        // ---- which columns see this thread's key: lane c collects column c's
+        // bits for the warp's 32 keys, then the warp transposes
+        const bool tail = t * kTile + kTile > ctx;      // the tile holds nodes
+        uint32_t sees = kAll;
+        if (tail) {
+          const int j0 = t * kTile + 32 * wq - ctx;     // node of the warp's first key
+          uint32_t bits = j0 < 0 ? low_bits(-j0) : 0;
+          if (my_node >= 0 && j0 > -32 && j0 < seg.n) {
+            uint32_t m;
+            if (a.mask)
+              m = mask_bits(my_mask, a.mask_words, j0) & low_bits(seg.n - j0);
+            else
+              m = my_node < j0 ? 0u : low_bits(my_node - j0 + 1);
+            bits |= m;
+          }
+          sees = transpose_bits(bits, lane);
         }
 
         // ---- scores, in log2 units against the reference
-        ok = ok && mbar_wait(&ctl.s_full[g & 1], (g >> 1) & 1, abort_flag);
+        wait_warp(&ctl.s_full[g % C::kSRing], (g / C::kSRing) & 1);
         tc_fence_after();
-        float x[C::kHalf];
+        float x[kCols];
         {
-          uint32_t u[C::kHalf];
-          tmem_ld<C::kHalf>(t_s + (g & 1) * C::kN, u);
+          uint32_t u[kCols];
+          tmem_ld<kCols>(t_s + (g & 1) * C::kN, u);
           if constexpr (kFp8) {
-            uint32_t v[C::kHalf];
-            tmem_ld<C::kHalf>(t_s + (g & 1) * C::kN + R, v);
-            tmem_ld_wait();
 #pragma unroll
-            for (int c = 0; c < C::kHalf; ++c)
-              x[c] = fmaf(__uint_as_float(v[c]), 0.0625f, __uint_as_float(u[c]));
+            for (int h = 0; h < kCols; h += kPart) {
+              uint32_t v[kPart];
+              tmem_ld<kPart>(t_s + (g & 1) * C::kN + R + h, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int c = 0; c < kPart; ++c)
+                x[h + c] = fmaf(__uint_as_float(v[c]), 0.0625f, __uint_as_float(u[h + c]));
+            }
           } else {
             tmem_ld_wait();
 #pragma unroll
-            for (int c = 0; c < C::kHalf; ++c) x[c] = __uint_as_float(u[c]);
+            for (int c = 0; c < kCols; ++c) x[c] = __uint_as_float(u[c]);
           }
         }
-        tc_fence_before();
-        mbar_arrive(&ctl.s_free[g & 1]);
         float top = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < C::kHalf; ++c) {
-          const float f = kFp8 ? ctl.factor[par][col0 + c] : unit_factor;
-          x[c] = fmaf(x[c], f, off[c]);
+        for (int c = 0; c < kCols; c += 2) {
+          const float4 s4 = *reinterpret_cast<const float4*>(&col.scale[col0 + c]);
+          x[c] = fmaf(x[c], s4.x, s4.y);
+          x[c + 1] = fmaf(x[c + 1], s4.z, s4.w);
         }
         if (tail) {
 #pragma unroll
-          for (int c = 0; c < C::kHalf; ++c)
-            if (j >= 0 && !sees(c, j)) x[c] = -INFINITY;
+          for (int c = 0; c < kCols; ++c)
+            if (!(sees >> c & 1u)) x[c] = -INFINITY;
         }
 #pragma unroll
-        for (int c = 0; c < C::kHalf; ++c) top = fmaxf(top, x[c]);
+        for (int c = 0; c < kCols; c += 2) top = fmax3(top, x[c], x[c + 1]);
 
         // ---- does the reference of a column move?
         if (group_any(bar_wg, unset != 0 || top > kPOffset + kRefLag)) {
+          float v[kCols];
 #pragma unroll
-          for (int c = 0; c < C::kHalf; ++c) {
-            const float m = warp_max(x[c]);
-            if (lane == 0) ctl.red[wg][c][wq] = m;
-          }
+          for (int c = 0; c < kCols; ++c) v[c] = x[c];
+          const float mine = reduce_columns<kCols, true>(v, lane);
+          if (lane < kCols) ctl.top[wg][wq][lane] = mine;
           group_sync(bar_wg, 128);
-          bool rescale = false;
-          float scale[C::kHalf];
-#pragma unroll
-          for (int c = 0; c < C::kHalf; ++c) {
-            const float4 m4 = *reinterpret_cast<const float4*>(ctl.red[wg][c]);
-            const float m = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
-            const bool fresh = (unset >> c & 1u) != 0;
-            scale[c] = 1.0f;
-            if (fresh ? m > -INFINITY : m > kPOffset + kRefLag) {
-              const float by = kPOffset - m;
-              off[c] += by;
-              x[c] += by;
-              if (!fresh) {
-                scale[c] = ex2_approx(by);
-                sum[c] *= scale[c];
-                rescale = true;
-              }
-              unset &= ~(1u << c);
-            }
+          // lane c decides for column c; all four warps come to the same
+          const float m = fmaxf(fmaxf(ctl.top[wg][0][c_mine], ctl.top[wg][1][c_mine]),
+                                fmaxf(ctl.top[wg][2][c_mine], ctl.top[wg][3][c_mine]));
+          const bool fresh = (unset >> c_mine & 1u) != 0;
+          const bool moves = fresh ? m > -INFINITY : m > kPOffset + kRefLag;
+          const float by = moves ? kPOffset - m : 0.0f;
+          const uint32_t moved = __ballot_sync(0xffffffffu, moves) & kAll;
+          my_off += by;
+          if (lane < kCols) {
+            col.scale[col0 + lane].y = my_off;
+            ctl.bc[warp][0][lane] = by;
+            ctl.bc[warp][1][lane] = fresh ? 1.0f : ex2_approx(by);
           }
-          // the same for all 128 threads; an unset column's O^T is zero
+          __syncwarp();
+          const bool rescale = (moved & ~unset) != 0;   // an unset column's O^T is zero
+          unset &= ~moved;
+#pragma unroll
+          for (int c = 0; c < kCols; c += 4) {
+            const float4 b4 = *reinterpret_cast<const float4*>(&ctl.bc[warp][0][c]);
+            const float4 s4 = *reinterpret_cast<const float4*>(&ctl.bc[warp][1][c]);
+            x[c] += b4.x, x[c + 1] += b4.y, x[c + 2] += b4.z, x[c + 3] += b4.w;
+            sum[c] *= s4.x, sum[c + 1] *= s4.y, sum[c + 2] *= s4.z, sum[c + 3] *= s4.w;
+          }
           if (rescale) {
-            ok = ok && mbar_wait(&ctl.pv_done, (g - 1) & 1, abort_flag);
+            wait_pv(g - 1);
             tc_fence_after();
-            uint32_t o[C::kHalf];
-            tmem_ld<C::kHalf>(t_o, o);
+            uint32_t o[kCols];
+            tmem_ld<kCols>(t_o, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int c = 0; c < C::kHalf; ++c)
-              o[c] = __float_as_uint(__uint_as_float(o[c]) * scale[c]);
-            tmem_st<C::kHalf>(t_o, o);
+            for (int c = 0; c < kCols; ++c)
+              o[c] = __float_as_uint(__uint_as_float(o[c]) * ctl.bc[warp][1][c]);
+            tmem_st<kCols>(t_o, o);
             tmem_st_wait();
           }
-          group_sync(bar_wg, 128);   // `red` may be written again
+          __syncwarp();   // `bc` may be written again
         }
 
         // ---- P
-        uint32_t w[C::kHalf / 2];
+        uint32_t w[kCols / 2];
 #pragma unroll
-        for (int c = 0; c < C::kHalf; c += 2) {
+        for (int c = 0; c < kCols; c += 2) {
           const float p0 = ex2_approx(x[c]), p1 = ex2_approx(x[c + 1]);
           sum[c] += p0;
           sum[c + 1] += p1;
           w[c / 2] = kFp8 ? cvt_f16x2(p0, p1) : cvt_bf16x2(p0, p1);
         }
-        if (g > 0) ok = ok && mbar_wait(&ctl.pv_done, (g - 1) & 1, abort_flag);
+        if (g > 0) wait_pv(g - 1);
 #pragma unroll
-        for (int i = 0; i < C::kHalf / 8; ++i)
-          *reinterpret_cast<uint4*>(prow + (((col0 / 8 + i) ^ (key & 7)) << 4)) =
+        for (int i = 0; i < kCols / 8; ++i)
+          *reinterpret_cast<uint4*>(prow + (((col0 / 8 + i) ^ pswz) << 4)) =
               make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
         fence_proxy_async();
         tc_fence_before();
-        mbar_arrive(&ctl.p_full);
+        arrive_warp(&ctl.p_full);
       }
 
       // ---- epilogue: lane = channel
-      const int n_rows = seg.n * a.group - seg.rt * R;   // live columns of the tile
-      const float mine = column_sum<C::kHalf>(sum, lane);
-      if (lane < C::kHalf) ctl.red[wg][lane][wq] = mine;
-      ok = ok && mbar_wait(&ctl.pv_done, (g - 1) & 1, abort_flag);
+      const float mine = reduce_columns<kCols, false>(sum, lane);
+      if (lane < kCols) ctl.sum[wg][wq][lane] = mine;
+      wait_pv(g - 1);
       tc_fence_after();
-      float o[C::kHalf];
+      float o[kCols];
       {
-        uint32_t u[C::kHalf];
-        tmem_ld<C::kHalf>(t_o, u);
+        uint32_t u[kCols];
+        tmem_ld<kCols>(t_o, u);
         tmem_ld_wait();
 #pragma unroll
-        for (int c = 0; c < C::kHalf; ++c) o[c] = __uint_as_float(u[c]);
+        for (int c = 0; c < kCols; ++c) o[c] = __uint_as_float(u[c]);
       }
       tc_fence_before();
-      group_sync(3, kSoftmaxThreads);   // sums and `flagged` are in place
-      if (ctl.flagged[par]) {
-        const int head = seg.head;
+      group_sync(bar_wg, 128);   // the sums are in place
+      if (*const_cast<volatile int*>(&ctl.flagged[(unit + 1) & 3]) == unit + 1) {
         for (int pos = max(ctx, seg.t0 * kTile); pos < min(seg.seq, seg.t1 * kTile); ++pos) {
           const int id = a.tables[seg.b * a.table_stride + (pos >> a.page_log2)];
           if (id < 0 || id >= a.num_pages) continue;
-          const float v = v_value<kFp8>(
-              a.v, id * a.page_stride + (pos & ((1 << a.page_log2) - 1)) * a.slot_stride +
-                       head * a.head_stride + key);
-          if ((__float_as_uint(v) & 0x7F800000u) != 0x7F800000u) continue;
+          const int64_t at = id * a.page_stride +
+                             (pos & ((1 << a.page_log2) - 1)) * a.slot_stride +
+                             seg.head * a.head_stride + key;
+          const int j = pos - ctx;
+          const bool mine_sees =
+              my_node >= 0 &&
+              (a.mask ? (__ldg(my_mask + (j >> 6)) >> (j & 63) & 1) != 0 : j <= my_node);
+          const uint32_t who = __ballot_sync(0xffffffffu, mine_sees);
+          float v = 0.0f;
+          if (kFp8) {
+            if ((a.v[at] & 0x7Fu) == 0x7Fu) v = __uint_as_float(0x7FC00000u);
+          } else {
+            const uint32_t u = reinterpret_cast<const uint16_t*>(a.v)[at];
+            if ((u & 0x7F80u) == 0x7F80u) v = __uint_as_float(u << 16);
+          }
 #pragma unroll
-          for (int c = 0; c < C::kHalf; ++c)
-            if (sees(c, pos - ctx)) o[c] += v;
+          for (int c = 0; c < kCols; ++c)
+            if (who >> c & 1u) o[c] += v;
         }
       }
-      const bool live = ok && !*abort_flag;
+      const float l = (ctl.sum[wg][0][c_mine] + ctl.sum[wg][1][c_mine]) +
+                      (ctl.sum[wg][2][c_mine] + ctl.sum[wg][3][c_mine]);
       if (seg.t0 == 0 && seg.t1 == seg.tiles) {
+        // through shared memory (P's place): rows of 256 bytes, 16 bytes a thread
+        if (lane < kCols) ctl.bc[warp][0][lane] = l == 0.0f ? 0.0f : ds_v / l;
+        __syncwarp();
+        uint8_t* stage = sp + col0 * 256;
 #pragma unroll
-        for (int c = 0; c < C::kHalf; ++c) {
-          const float4 s4 = *reinterpret_cast<const float4*>(ctl.red[wg][c]);
-          const float l = (s4.x + s4.y) + (s4.z + s4.w);
-          const int row = ctl.out_row[par][col0 + c];
-          if (live && row >= 0)
-            a.out[static_cast<int64_t>(row) * kHeadDim + key] =
-                __float2bfloat16(l == 0.0f ? 0.0f : o[c] * (ds_v / l));
+        for (int c = 0; c < kCols; c += 4) {
+          const float4 s4 = *reinterpret_cast<const float4*>(&ctl.bc[warp][0][c]);
+          const float sc[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            reinterpret_cast<__nv_bfloat16*>(stage + (c + u) * 256)[key] =
+                __float2bfloat16(sc[u] == 0.0f ? 0.0f : o[c + u] * sc[u]);
         }
-      } else {
-        const int64_t piece = 2 * static_cast<int64_t>(blockIdx.x) + (seg.t0 == 0);
+        // (the whole group: its threads are 32 wq + lane = key)
+        group_sync(bar_wg, 128);
+        if (!*abort_flag) {
 #pragma unroll
-        for (int c = 0; c < C::kHalf; ++c) {
-          const float4 s4 = *reinterpret_cast<const float4*>(ctl.red[wg][c]);
-          const int64_t at = piece * R + col0 + c;
-          if (live && col0 + c < n_rows) {
-            a.part_o[at * kHeadDim + key] = o[c];
-            if (key == 0)
-              a.part_ml[at] = make_float2((unset >> c & 1u) ? -INFINITY : kPOffset - off[c],
-                                          (s4.x + s4.y) + (s4.z + s4.w));
+          for (int it = 0; it < kCols / 8; ++it) {
+            const int r = it * 8 + (key >> 4), c = key & 15;
+            const int row = col.out_row[col0 + r];
+            if (row >= 0)
+              reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(row) * kHeadDim)[c] =
+                  *reinterpret_cast<const uint4*>(stage + r * 256 + c * 16);
           }
         }
+        group_sync(3, C::kSoftmaxThreads);   // P may be written again
+      } else if (!*abort_flag) {
+        const int64_t piece = (2 * static_cast<int64_t>(blockIdx.x) + (seg.t0 == 0)) * R + col0;
+        const int live = seg.n * a.group - seg.rt * R - col0;   // live columns of this group
+        float* to = a.part_o + piece * kHeadDim + key;
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+          if (c < live) to[c * kHeadDim] = o[c];
+        if (wq == 0 && lane < kCols && lane < live)
+          a.part_ml[piece + lane] =
+              make_float2((unset >> lane & 1u) ? -INFINITY : kPOffset - my_off, l);
       }
-    }
-    if (!ok) {
-      ctl.abort_flag = 1;
-      raise_error(a.err, kErrTimeout);
+      __syncwarp();   // `bc` may be written again
     }
   }
 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+  if (warp == C::kMmaWarp) tmem_dealloc(tmem, C::kTmem);
 }
 
 // ---------------------------------------------------------------------------
@@ -827,51 +1008,75 @@ kv_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
 // ---------------------------------------------------------------------------
 
 constexpr int kJoinThreads = 256;
-constexpr int kJoinRows = 8;
+constexpr int kJoinRows = kJoinThreads / 32;
 
 template <int R, bool kFp8>
 __global__ void __launch_bounds__(kJoinThreads) kv_tree_join_kernel(const TreeArgs a, int ctas) {
-  extern __shared__ int32_t prefix[];
+  __shared__ int chunk[kJoinThreads + 1];
   __shared__ int warp_sums[kJoinThreads / 32];
-  bool bad = false;
-  scan_requests<kJoinThreads>(a, R, prefix, warp_sums, &bad);
-  const int total = prefix[a.rows];
+  __shared__ float s_scale[kJoinRows][kMaxCtas];
+  __shared__ float s_inv[kJoinRows];
+  // everything up to the wait needs the lengths alone
+  scan_requests<R, kJoinThreads>(a, chunk, warp_sums);
+  __syncthreads();
+  const int total = chunk[kJoinThreads];
   const int per = tiles_per_cta(total, ctas);
   const int64_t border = static_cast<int64_t>(blockIdx.x + 1) * per;
+  Finder<R, kJoinThreads> find;
+  const Request& q = find.r;
+  const int w = static_cast<int>(min(border, static_cast<int64_t>(total)));
+  int unit = 0, c0 = -1, c1 = -1;     // the unit at the border, and its CTAs
+  if (w < total) {
+    find.seek(a, chunk, w);
+    unit = (w - find.start) / q.tiles;
+    const int from = find.start + unit * q.tiles;
+    if (from < w) {
+      c0 = from / per;
+      c1 = (from + q.tiles - 1) / per;
+    }
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (border >= total) return;
-  const int w = static_cast<int>(border);
-  const int b = request_of(prefix, a.rows, w);
-  const int q0 = a.cu[b], n = a.cu[b + 1] - q0, tiles = (a.seq[b] + kTile - 1) / kTile;
-  const int rts = row_tiles(n, a.group, R);
-  const int unit = (w - prefix[b]) / tiles;
-  const int from = prefix[b] + unit * tiles, to = from + tiles;
-  const int c0 = from / per, c1 = (to - 1) / per;   // its CTAs
-  if (from == w || c0 != static_cast<int>(blockIdx.x)) return;
-  const int head = unit / rts, rt = unit - head * rts;
-  const float ds_v = kFp8 ? __ldg(a.descale + 2) : 1.0f;
-  const int d = threadIdx.x & 127;
-  for (int i = threadIdx.x >> 7; i < kJoinRows; i += kJoinThreads / 128) {
-    const int r = blockIdx.y * kJoinRows + i;
-    const int row = rt * R + r;
-    const int node = row / a.group;
-    if (node >= n) continue;
+  if (c0 != static_cast<int>(blockIdx.x)) return;   // none, or an earlier border's
+  const int head = unit / q.row_tiles, rt = unit - head * q.row_tiles;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int pieces = c1 - c0 + 1;
+  // piece i of row r; the first CTA's piece is its last one, the others' their first
+  auto at = [&](int i, int r) {
+    return (2 * static_cast<int64_t>(c0 + i) + (i == 0)) * R + blockIdx.y * kJoinRows + r;
+  };
+  // a warp per row: the pieces' weights
+  {
     float m = -INFINITY;
-    for (int c = c0; c <= c1; ++c)
-      m = fmaxf(m, a.part_ml[(2 * static_cast<int64_t>(c) + (c == c0)) * R + r].x);
-    float o = 0.0f, l = 0.0f;
-    for (int c = c0; c <= c1; ++c) {
-      const int64_t at = (2 * static_cast<int64_t>(c) + (c == c0)) * R + r;
-      const float2 ml = a.part_ml[at];
+    for (int i = lane; i < pieces; i += 32) m = fmaxf(m, a.part_ml[at(i, warp)].x);
+#pragma unroll
+    for (int off = 16; off >= 1; off /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    float l = 0.0f;
+    for (int i = lane; i < pieces; i += 32) {
+      const float2 ml = a.part_ml[at(i, warp)];
       // a piece of no visible key has ref = -inf, O = 0 and l = 0; one whose
       // scores were all NaN has ref = -inf and l = NaN
       const float scale = ml.x == -INFINITY ? 1.0f : exp2f(ml.x - m);
-      o = fmaf(scale, a.part_o[at * kHeadDim + d], o);
+      s_scale[warp][i] = scale;
       l = fmaf(scale, ml.y, l);
     }
-    const int64_t out_row = static_cast<int64_t>(q0 + node) * (a.kv_heads * a.group) +
+#pragma unroll
+    for (int off = 16; off >= 1; off /= 2) l += __shfl_xor_sync(0xffffffffu, l, off);
+    if (lane == 0) s_inv[warp] = l == 0.0f ? 0.0f : (kFp8 ? __ldg(a.descale + 2) : 1.0f) / l;
+  }
+  __syncthreads();
+  const int d = threadIdx.x & 127;
+  for (int r = threadIdx.x >> 7; r < kJoinRows; r += kJoinThreads / 128) {
+    const int row = rt * R + blockIdx.y * kJoinRows + r;
+    const int node = row / a.group;
+    if (node >= q.n) continue;
+    float o = 0.0f;
+#pragma unroll 8
+    for (int i = 0; i < pieces; ++i)
+      o = fmaf(s_scale[r][i], a.part_o[at(i, r) * kHeadDim + d], o);
+    const int64_t out_row = static_cast<int64_t>(q.q0 + node) * (a.kv_heads * a.group) +
                             head * a.group + (row - node * a.group);
-    a.out[out_row * kHeadDim + d] = __float2bfloat16(l == 0.0f ? 0.0f : o * (ds_v / l));
+    const float inv = s_inv[r];
+    a.out[out_row * kHeadDim + d] = __float2bfloat16(inv == 0.0f ? 0.0f : o * inv);
   }
 }
 
@@ -918,7 +1123,6 @@ bool make_cache_map(CUtensorMap* m, const void* base, const PagedCache& c) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr int kMaxCtas = 148;   // one per SM
 
 // Query rows of a tile: the fewest columns that hold a request's rows of a KV
 // head (16 is the smallest N; above 64 a request takes several row tiles).
@@ -939,10 +1143,8 @@ cudaError_t launch_t(const KvTreeLaunch& p, const TreeArgs& a, cudaStream_t stre
   CUtensorMap mk, mv;
   if (!make_cache_map(&mk, p.cache.k, p.cache) || !make_cache_map(&mv, p.cache.v, p.cache))
     return cudaErrorInvalidValue;
-  const int prefix_bytes = (p.rows + 1) * static_cast<int>(sizeof(int32_t));
-  constexpr int kBase = 1024 + C::kSmemData + static_cast<int>(sizeof(Control));
-  constexpr int kMost = kBase + (kMaxTreeRows + 1) * static_cast<int>(sizeof(int32_t));
-  static_assert(kMost <= 232448, "shared memory of a CTA");
+  constexpr int kSmem = 1024 + C::kSmemData + static_cast<int>(sizeof(Control<R, kFp8>));
+  static_assert(kSmem <= 232448, "shared memory of a CTA");
   static std::mutex mu;
   static uint64_t attr_set = 0;   // bit d: done on device d (one per instantiation)
   {
@@ -953,20 +1155,19 @@ cudaError_t launch_t(const KvTreeLaunch& p, const TreeArgs& a, cudaStream_t stre
     std::lock_guard<std::mutex> lock(mu);
     if (!(attr_set >> dev & 1u)) {
       e = cudaFuncSetAttribute(kv_tree_kernel<R, kFp8>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
       if (e != cudaSuccess) return e;
       attr_set |= uint64_t{1} << dev;
     }
   }
   const int ctas = launch_ctas(p.rows, p.max_q, p.max_seqlen, p.heads, p.cache.heads);
-  kv_tree_kernel<R, kFp8><<<ctas, kThreads, kBase + prefix_bytes, stream>>>(mk, mv, a);
+  kv_tree_kernel<R, kFp8><<<ctas, C::kThreads, kSmem, stream>>>(mk, mv, a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || ctas == 1) return e;
   note_launch();   // the caller counts one launch
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas - 1), R / kJoinRows);
   cfg.blockDim = dim3(kJoinThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(prefix_bytes);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

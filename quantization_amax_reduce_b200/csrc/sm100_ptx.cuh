@@ -257,6 +257,19 @@ __host__ __device__ constexpr uint32_t make_idesc(uint32_t a_fmt, uint32_t b_fmt
 // An instruction descriptor's A operand taken MN-major (transposed).
 constexpr uint32_t kIdescAMnMajor = 1u << 15;
 
+// Swizzling modes of a shared-memory matrix descriptor.
+constexpr uint64_t kSwizzle128 = 2, kSwizzle64 = 4, kSwizzle32 = 6;
+
+// Shared-memory matrix descriptor of a swizzling mode (lbo and sbo as below).
+__device__ __forceinline__ uint64_t make_sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo,
+                                               uint64_t mode) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) |
+         static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16 |
+         static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32 |
+         static_cast<uint64_t>(1u) << 46 |  // descriptor version (sm_100)
+         mode << 61;
+}
+
 // Shared-memory matrix descriptor with 128-byte swizzling.
 //   lbo: byte offset between swizzle atoms along MN (MN-major operands)
 //   sbo: byte offset between 8-row groups (K-major: along MN; MN-major: along K)
@@ -449,13 +462,6 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
-// The warp's maximum of one value per lane (NaN lanes are left out).
-__device__ __forceinline__ float warp_max(float x) {
-  float d;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(d) : "f"(x));
   return d;
 }
 
