@@ -559,15 +559,20 @@ def read_error_word(error: torch.Tensor, stream=None) -> int:
 # paged KV cache
 # ---------------------------------------------------------------------------
 
+_HERE = contextlib.nullcontext()
+
+
 def _launch_on(stream, device):
     """(handle, context manager): the stream of a call and a context in which
     the call's device is current and torch allocates on that stream, so that
     neither its outputs nor its workspace are memory that another stream's
     pending work still uses."""
     if stream is None:
-        if device.index == torch.cuda.current_device():
-            return torch.cuda.current_stream(device).cuda_stream, contextlib.nullcontext()
-        return torch.cuda.current_stream(device).cuda_stream, torch.cuda.device(device)
+        # (the raw handle: torch.cuda.current_stream builds an object for 2 us)
+        handle = torch._C._cuda_getCurrentRawStream(device.index)
+        if device.index == torch._C._cuda_getDevice():
+            return handle, _HERE
+        return handle, torch.cuda.device(device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) \
             else torch.cuda.default_stream(device)
@@ -662,12 +667,9 @@ def kv_assign_pages(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_tables
     handle, on = _launch_on(stream, dev)
     with on:
         if out is None:
-            # one allocation: slots, positions, cu (slots and positions 16-byte aligned)
-            n8, n4 = 8 * max_tokens + 15 & ~15, 4 * max_tokens + 15 & ~15
-            buf = torch.empty(n8 + n4 + 4 * rows + 4, dtype=torch.uint8, device=dev)
-            slots = buf[:8 * max_tokens].view(torch.int64)
-            positions = buf[n8:n8 + 4 * max_tokens].view(torch.int32)
-            cu = buf[n8 + n4:].view(torch.int32)
+            cu = seq_lens.new_empty(rows + 1)
+            slots = seq_lens.new_empty(max_tokens, dtype=torch.int64)
+            positions = seq_lens.new_empty(max_tokens)
         else:
             cu, slots, positions = out
             _check_out(cu, "cu_new", torch.int32, rows + 1, dev)
@@ -764,10 +766,10 @@ def kv_tree_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     handle, on = _launch_on(stream, dev)
     with on:
         if out is None:
-            out = torch.empty((T, heads, HEAD_DIM), dtype=torch.bfloat16, device=dev)
+            out = q.new_empty(q.shape)
         else:
             _check_out(out, "out", torch.bfloat16, T * heads * HEAD_DIM, dev)
-        work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        work = seq_lens.new_empty(need + 3 >> 2) if need else None
         _check(L.fp8attn_kv_tree_fwd(
             q.data_ptr(), tok_stride, head_stride, k_cache.data_ptr(), v_cache.data_ptr(),
             strides[0], strides[1], strides[2], pages, page_size, tables, table_stride, width,

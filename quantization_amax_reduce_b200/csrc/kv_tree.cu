@@ -19,10 +19,10 @@
 //
 //   warps 0-3, 4-7: two groups of 128 threads, each with half of the columns:
 //               softmax, P, epilogue
-//   warp 8      TMA producer: rings of K and V tiles, a box per page (page ids
-//               from the block table, one lane per page)
-//   warp 9      MMA issuer: S^T(t+1), then O^T += V^T P^T(t)
-//   warps 10-13 the next unit's Q into shared memory; V: E4M3 -> f16 into the
+//   warps 8, 9  TMA producers of K and of V: rings of tiles, a box per page
+//               (page ids from the block table, one lane per page)
+//   warp 10     MMA issuer: S^T(t+1), then O^T += V^T P^T(t)
+//   warps 11-14 the next unit's Q into shared memory; V: E4M3 -> f16 into the
 //               buffer that the product reads, and the rows that must not touch
 //               it (past the sequence, non-finite)
 // One lane of a warp waits and arrives for it: 256 threads that each try the
@@ -80,7 +80,7 @@ struct Cfg {
   static constexpr int kGroups = 2;
   static constexpr int kCols = R / kGroups;               // columns of a softmax thread
   static constexpr int kSoftmaxWarps = 4 * kGroups, kSoftmaxThreads = 128 * kGroups;
-  static constexpr int kTmaWarp = kSoftmaxWarps, kMmaWarp = kTmaWarp + 1;
+  static constexpr int kTmaWarp = kSoftmaxWarps, kMmaWarp = kTmaWarp + 2;   // K, V; products
   static constexpr int kPrepWarp = kMmaWarp + 1, kPrepWarps = 4;
   static constexpr int kThreads = 32 * (kPrepWarp + kPrepWarps);
   static constexpr int kN = kFp8 ? 2 * R : R;             // columns of S^T
@@ -134,7 +134,8 @@ struct Segment {
 // u + 2's slot is written.
 template <int R>
 struct Columns {
-  alignas(16) float2 scale[R];           // {S^T -> log2 units, kPOffset - ref}
+  alignas(16) float factor[R];           // S^T -> log2 units
+  alignas(16) float off[R];              // kPOffset - ref, 0 while unset
   int out_row[R];                        // row of `out`, -1 = none
   int node[R];                           // -1 = none
   Segment seg;
@@ -399,10 +400,8 @@ kv_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     ctl.abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == C::kTmaWarp && lane == 0) {
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
-  }
+  if (warp == C::kTmaWarp && lane == 0) tma_prefetch_desc(&tm_k);
+  if (warp == C::kTmaWarp + 1 && lane == 0) tma_prefetch_desc(&tm_v);
   if (warp == C::kMmaWarp) {
     tmem_alloc(&ctl.tmem_base, C::kTmem);
     tmem_relinquish();
@@ -414,11 +413,12 @@ kv_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   tc_fence_after();
   const uint32_t tmem = ctl.tmem_base;
   const volatile int* abort_flag = &ctl.abort_flag;
-  // One lane waits and arrives for its warp.  A wait that gives up sets the
-  // abort flag, which ends all other waits at once; the roles then run on
-  // without data (so that every barrier is met) and write no output.
+  // A wait that gives up sets the abort flag, which ends all other waits at
+  // once; the roles then run on without data (so that every barrier is met)
+  // and write no output.  (The whole warp tests: 64 cycles when the phase is
+  // over already, against 117 for one lane and a warp sync.)
   auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
-    if (lane == 0 && !mbar_wait(bar, parity, abort_flag)) {
+    if (!mbar_wait(bar, parity, abort_flag)) {
       if (!*abort_flag) raise_error(a.err, kErrTimeout);
       ctl.abort_flag = 1;
     }
@@ -436,15 +436,21 @@ kv_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     return s.t0 < s.t1 && !*abort_flag;
   };
 
-  if (warp == C::kTmaWarp) {
-    // ------------------------------------------------------------ producer
+  if (warp < C::kMmaWarp && warp >= C::kTmaWarp) {
+    // ------------------------------------------------------------ producers
+    // of K (the first warp) and V: neither waits for the other's stages
+    const bool is_k = warp == C::kTmaWarp;
+    const CUtensorMap* map = is_k ? &tm_k : &tm_v;
+    uint8_t* ring = is_k ? sk : sv;
+    uint64_t* full = is_k ? ctl.k_full : ctl.v_full;
+    const int stages = is_k ? C::kKStages : C::kVStages;
     const int page = 1 << a.page_log2;
     const int box = min(page, kTile);
     const int box_log2 = min(a.page_log2, 7);
     Walker<R, C::kThreads> walk;
     walk.init(ctl.chunk, gridDim.x);
     Segment seg;
-    int g = 0;
+    int g = 0, stage = 0, turn = 0;
     while (!*abort_flag && walk.next(a, ctl.chunk, seg)) {
       const int32_t* table = a.tables + seg.b * a.table_stride;
       // the page of this lane's box of tile t, looked up a tile ahead
@@ -458,42 +464,35 @@ kv_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         const int id = next_id;
         if (t + 1 < seg.t1) next_id = look_up(t + 1);
         const bool load = id != -2;
-        if (load && (id < 0 || id >= a.num_pages)) raise_error(a.err, kErrPages);
+        if (is_k && load && (id < 0 || id >= a.num_pages)) raise_error(a.err, kErrPages);
         const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, load)) * box * (kFp8 ? 128 : 256);
         const int row = a.page_log2 > 7 ? (t * kTile) & (page - 1) : 0;
-        const int ks = g % C::kKStages, vs = g % C::kVStages;
         // a page id outside the cache is outside the tensor map: zeros arrive;
         // after an abort the copies go on, into stages that nobody reads
-        const int freed = g - C::kKStages;      // its S^T frees the stage
-        if (freed >= 0) wait_warp(&ctl.s_full[freed % C::kSRing], (freed / C::kSRing) & 1);
-        if (lane == 0) mbar_expect_tx(&ctl.k_full[ks], bytes);
+        if (turn > 0) {
+          if (is_k) {        // its S^T frees a K stage
+            const int freed = g - C::kKStages;
+            wait_warp(&ctl.s_full[freed % C::kSRing], (freed / C::kSRing) & 1);
+          } else {           // the preparing warps, and O^T, free a V stage
+            wait_warp(&ctl.v_empty[stage], (turn - 1) & 1);
+            if (!kFp8) wait_pv(g - C::kVStages);
+          }
+        }
+        if (lane == 0) mbar_expect_tx(&full[stage], bytes);
         __syncwarp();
         if (load) {
-          uint8_t* dst = sk + ks * C::kKV + lane * box * 128;
-          tma_load_4d(dst, &tm_k, &ctl.k_full[ks], 0, seg.head, row, id);
-          if (!kFp8) tma_load_4d(dst + 16384, &tm_k, &ctl.k_full[ks], 64, seg.head, row, id);
-        }
-        if (g >= C::kVStages) {
-          wait_warp(&ctl.v_empty[vs], (g / C::kVStages - 1) & 1);
-          if (!kFp8) wait_pv(g - C::kVStages);
-        }
-        if (lane == 0) mbar_expect_tx(&ctl.v_full[vs], bytes);
-        __syncwarp();
-        if (load) {
-          uint8_t* dst = sv + vs * C::kKV + lane * box * 128;
-          tma_load_4d(dst, &tm_v, &ctl.v_full[vs], 0, seg.head, row, id);
-          if (!kFp8) tma_load_4d(dst + 16384, &tm_v, &ctl.v_full[vs], 64, seg.head, row, id);
+          uint8_t* dst = ring + stage * C::kKV + lane * box * 128;
+          tma_load_4d(dst, map, &full[stage], 0, seg.head, row, id);
+          if (!kFp8) tma_load_4d(dst + 16384, map, &full[stage], 64, seg.head, row, id);
         }
         __syncwarp();
+        if (++stage == stages) stage = 0, ++turn;
       }
     }
     // no copy may still be landing when the CTA leaves
-    if (lane == 0) {
-      for (int i = max(0, g - C::kKStages); i < g; ++i)
-        mbar_wait(&ctl.k_full[i % C::kKStages], (i / C::kKStages) & 1, nullptr);
-      for (int i = max(0, g - C::kVStages); i < g; ++i)
-        mbar_wait(&ctl.v_full[i % C::kVStages], (i / C::kVStages) & 1, nullptr);
-    }
+    if (lane == 0)
+      for (int i = max(0, g - stages); i < g; ++i)
+        mbar_wait(&full[i % stages], (i / stages) & 1, nullptr);
     __syncwarp();
   } else if (warp == C::kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
@@ -637,7 +636,10 @@ kv_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           *reinterpret_cast<uint4*>(sq + (c >> 3) * (R * 128) + (r >> 3) * 1024 + (r & 7) * 128 +
                                     (((c & 7) ^ (r & 7)) << 4)) = x;
         }
-        if (c == 0) col.scale[r] = make_float2(factor, 0.0f);
+        if (c == 0) {
+          col.factor[r] = factor;
+          col.off[r] = 0.0f;
+        }
       }
       if (tid < R) {
         const int row = s.rt * R + tid;
@@ -779,9 +781,9 @@ kv_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     for (int unit = 0; unit_at(unit, seg); ++unit) {
       Columns<R>& col = ctl.col[unit & 3];
       const int ctx = seg.seq - seg.n;
-      float sum[kCols];
+      uint64_t sum2[kCols / 2];   // row sums of this thread's keys, columns in pairs
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) sum[c] = 0.0f;
+      for (int c = 0; c < kCols / 2; ++c) sum2[c] = 0;
       const int my_node = col.node[col0 + c_mine];
       const unsigned long long* my_mask =
           a.mask + static_cast<int64_t>(seg.q0 + max(my_node, 0)) * a.mask_words;
@@ -811,40 +813,45 @@ kv_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         // ---- scores, in log2 units against the reference
         wait_warp(&ctl.s_full[g % C::kSRing], (g / C::kSRing) & 1);
         tc_fence_after();
-        float x[kCols];
+        // columns in pairs: x2[c / 2] = columns c, c + 1
+        uint64_t x2[kCols / 2];
         {
-          uint32_t u[kCols];
-          tmem_ld<kCols>(t_s + (g & 1) * C::kN, u);
-          if constexpr (kFp8) {
+          const uint64_t sixteenth = f2_pack(0.0625f, 0.0625f);
 #pragma unroll
-            for (int h = 0; h < kCols; h += kPart) {
-              uint32_t v[kPart];
-              tmem_ld<kPart>(t_s + (g & 1) * C::kN + R + h, v);
-              tmem_ld_wait();
-#pragma unroll
-              for (int c = 0; c < kPart; ++c)
-                x[h + c] = fmaf(__uint_as_float(v[c]), 0.0625f, __uint_as_float(u[h + c]));
-            }
-          } else {
+          for (int h = 0; h < kCols; h += kPart) {
+            uint32_t u[kPart], v[kPart];
+            tmem_ld<kPart>(t_s + (g & 1) * C::kN + h, u);
+            if (kFp8) tmem_ld<kPart>(t_s + (g & 1) * C::kN + R + h, v);
             tmem_ld_wait();
 #pragma unroll
-            for (int c = 0; c < kCols; ++c) x[c] = __uint_as_float(u[c]);
+            for (int c = 0; c < kPart; c += 4) {
+              const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(&col.factor[col0 + h + c]);
+              const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(&col.off[col0 + h + c]);
+              uint64_t lo = f2_bits(u[c], u[c + 1]), hi = f2_bits(u[c + 2], u[c + 3]);
+              if (kFp8) {
+                lo = f2_fma(f2_bits(v[c], v[c + 1]), sixteenth, lo);
+                hi = f2_fma(f2_bits(v[c + 2], v[c + 3]), sixteenth, hi);
+              }
+              x2[(h + c) / 2] = f2_fma(lo, f.x, o.x);
+              x2[(h + c) / 2 + 1] = f2_fma(hi, f.y, o.y);
+            }
           }
         }
-        float top = -INFINITY;
+        float x[kCols];
 #pragma unroll
-        for (int c = 0; c < kCols; c += 2) {
-          const float4 s4 = *reinterpret_cast<const float4*>(&col.scale[col0 + c]);
-          x[c] = fmaf(x[c], s4.x, s4.y);
-          x[c + 1] = fmaf(x[c + 1], s4.z, s4.w);
-        }
+        for (int c = 0; c < kCols; c += 2) f2_unpack(x2[c / 2], x[c], x[c + 1]);
         if (tail) {
 #pragma unroll
           for (int c = 0; c < kCols; ++c)
             if (!(sees >> c & 1u)) x[c] = -INFINITY;
         }
+        float top = -INFINITY;
+        {
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < kCols; c += 2) top = fmax3(top, x[c], x[c + 1]);
+          for (int c = 0; c < kCols; c += 2) m4[(c / 2) & 3] = fmax3(m4[(c / 2) & 3], x[c], x[c + 1]);
+          top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        }
 
         // ---- does the reference of a column move?
         if (group_any(bar_wg, unset != 0 || top > kPOffset + kRefLag)) {
@@ -863,7 +870,7 @@ kv_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
           const uint32_t moved = __ballot_sync(0xffffffffu, moves) & kAll;
           my_off += by;
           if (lane < kCols) {
-            col.scale[col0 + lane].y = my_off;
+            col.off[col0 + lane] = my_off;
             ctl.bc[warp][0][lane] = by;
             ctl.bc[warp][1][lane] = fresh ? 1.0f : ex2_approx(by);
           }
@@ -875,7 +882,8 @@ kv_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
             const float4 b4 = *reinterpret_cast<const float4*>(&ctl.bc[warp][0][c]);
             const float4 s4 = *reinterpret_cast<const float4*>(&ctl.bc[warp][1][c]);
             x[c] += b4.x, x[c + 1] += b4.y, x[c + 2] += b4.z, x[c + 3] += b4.w;
-            sum[c] *= s4.x, sum[c + 1] *= s4.y, sum[c + 2] *= s4.z, sum[c + 3] *= s4.w;
+            sum2[c / 2] = f2_mul(sum2[c / 2], f2_pack(s4.x, s4.y));
+            sum2[c / 2 + 1] = f2_mul(sum2[c / 2 + 1], f2_pack(s4.z, s4.w));
           }
           if (rescale) {
             wait_pv(g - 1);
@@ -897,8 +905,7 @@ kv_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
 #pragma unroll
         for (int c = 0; c < kCols; c += 2) {
           const float p0 = ex2_approx(x[c]), p1 = ex2_approx(x[c + 1]);
-          sum[c] += p0;
-          sum[c + 1] += p1;
+          sum2[c / 2] = f2_add(sum2[c / 2], f2_pack(p0, p1));
           w[c / 2] = kFp8 ? cvt_f16x2(p0, p1) : cvt_bf16x2(p0, p1);
         }
         if (g > 0) wait_pv(g - 1);
@@ -912,6 +919,9 @@ kv_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       }
 
       // ---- epilogue: lane = channel
+      float sum[kCols];
+#pragma unroll
+      for (int c = 0; c < kCols; c += 2) f2_unpack(sum2[c / 2], sum[c], sum[c + 1]);
       const float mine = reduce_columns<kCols, false>(sum, lane);
       if (lane < kCols) ctl.sum[wg][wq][lane] = mine;
       wait_pv(g - 1);
@@ -1117,9 +1127,13 @@ bool make_cache_map(CUtensorMap* m, const void* base, const PagedCache& c) {
   cuuint32_t box[4] = {static_cast<cuuint32_t>(c.fp8 ? 128 : 64), 1,
                        static_cast<cuuint32_t>(page < kTile ? page : kTile), 1};
   cuuint32_t es[4] = {1, 1, 1, 1};
+  // a 128-byte row of a token-major E4M3 page has another head's beside it,
+  // which this CTA does not read: no promotion past it
+  const bool beside = c.fp8 && c.slot_stride != kHeadDim;
   return fn(m, c.fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
             const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_SWIZZLE_128B,
+            beside ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
