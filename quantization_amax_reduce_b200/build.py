@@ -17,7 +17,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SOURCES = ["api.cu", "quant.cu", "attention.cu", "regroup.cu", "scale_map.cu",
            "kv_cache.cu", "kv_tree.cu"]
-HEADERS = ["kernels.h", "sm100_ptx.cuh", "state.cuh"]
+HEADERS = ["kernels.h", "kv_tree.cuh", "sm100_ptx.cuh", "state.cuh"]
 LIB = os.path.join(HERE, "libfp8attn.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 

@@ -1,0 +1,630 @@
+// Device code shared by the two attention kernels over the paged KV cache
+// (kv_tree.cu): arguments, the work list, the TMA producers and the warps that
+// prepare Q and V.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "sm100_ptx.cuh"
+#include "state.cuh"
+
+namespace fp8attn {
+
+namespace kv_tree {
+
+constexpr int kTile = 128;                 // keys of a tile
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kPOffset = 8.0f;           // log2 of P at the reference
+constexpr float kRefLag = 7.0f;
+// A CTA's range is at least this many tiles: below it another CTA and the
+// join of its piece cost more than the tiles they save.
+constexpr int kMinTiles = 4;
+constexpr int kMaxCtas = 148;              // one per SM
+constexpr int kPrepWarps = 4, kPrepThreads = 32 * kPrepWarps;
+
+struct TreeArgs {
+  const uint16_t* q;
+  int64_t q_tok_stride, q_head_stride;
+  const uint8_t* v;                      // V cache, for the non-finite rows
+  int64_t page_stride, slot_stride, head_stride;   // elements
+  int num_pages, page_log2, kv_heads, group;
+  const int32_t* tables;
+  int64_t table_stride;
+  int width;
+  const int32_t* seq;
+  const int32_t* cu;
+  int rows, max_q, max_seqlen, total_q;
+  const float* descale;
+  const unsigned long long* mask;
+  int mask_words;
+  float softmax_scale;
+  __nv_bfloat16* out;
+  float* part_o;                         // [2 CTAs][R][128]
+  float2* part_ml;                       // [2 CTAs][R] {ref, sum}
+  int32_t* err;
+};
+
+// A CTA's tiles [t0, t1) of one unit.
+struct Segment {
+  int b, head, rt;       // request, KV head, row tile
+  int seq, q0, n;
+  int tiles, t0, t1;     // tiles of the unit; this CTA's (none: the end)
+};
+
+// What a unit's rows stand for.  Units u and u + 1 may be in use while unit
+// u + 2's slot is written.
+template <int R>
+struct UnitRows {
+  alignas(16) float factor[R];           // score -> log2 units
+  int one_factor;                        // they are all the same
+  int out_row[R];                        // row of `out`, -1 = none
+  int node[R];                           // -1 = none
+  Segment seg;
+};
+
+__device__ __forceinline__ void raise_error(int32_t* err, uint32_t bits) {
+  if (err) atomicOr(reinterpret_cast<unsigned int*>(err), bits);
+}
+
+__device__ __forceinline__ void group_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// Does any of the group's 128 threads say yes?
+__device__ __forceinline__ bool group_any(int id, bool yes) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "bar.red.or.pred p, %2, 128, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(yes)), "r"(id)
+      : "memory");
+  return r != 0;
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
+  if constexpr (N == 8) tmem_ld8(taddr, r);
+  else if constexpr (N == 16) tmem_ld16(taddr, r);
+  else tmem_ld32(taddr, r);
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[N]) {
+  if constexpr (N == 8) tmem_st8(taddr, r);
+  else if constexpr (N == 16) tmem_st16(taddr, r);
+  else tmem_st32(taddr, r);
+}
+
+// Reduces N columns (a power of two up to 32) over the warp's lanes: lane l
+// gets column l % N.  N - 1 + log2(32 / N) shuffles instead of 5 N.
+template <int N, bool kMax>
+__device__ __forceinline__ float reduce_columns(float (&v)[N], int lane) {
+  auto join = [](float a, float b) { return kMax ? fmaxf(a, b) : a + b; };
+#pragma unroll
+  for (int off = N / 2; off >= 1; off /= 2) {
+    const bool up = (lane & off) != 0;
+#pragma unroll
+    for (int i = 0; i < off; ++i) {
+      const float send = up ? v[i] : v[i + off];
+      const float mine = up ? v[i + off] : v[i];
+      v[i] = join(mine, __shfl_xor_sync(0xffffffffu, send, off));
+    }
+  }
+#pragma unroll
+  for (int off = N; off < 32; off *= 2)
+    v[0] = join(v[0], __shfl_xor_sync(0xffffffffu, v[0], off));
+  return v[0];
+}
+
+// Transposes a 32 x 32 bit matrix held one row per lane.
+__device__ __forceinline__ uint32_t transpose_bits(uint32_t x, int lane) {
+  uint32_t m = 0x0000FFFFu;
+#pragma unroll
+  for (int j = 16; j >= 1; j >>= 1, m ^= m << j) {
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, x, j);
+    x = (lane & j) ? (x & ~m) | ((y >> j) & m) : (x & m) | ((y & m) << j);
+  }
+  return x;
+}
+
+// Bits [j0, j0 + 32) of a mask row of `words` words; j0 > -32.
+__device__ __forceinline__ uint32_t mask_bits(const unsigned long long* row, int words, int j0) {
+  if (j0 < 0) return static_cast<uint32_t>(__ldg(row) << -j0);
+  const int w = j0 >> 6, sh = j0 & 63;
+  if (w >= words) return 0;
+  uint64_t v = __ldg(row + w) >> sh;
+  if (sh > 32 && w + 1 < words) v |= __ldg(row + w + 1) << (64 - sh);
+  return static_cast<uint32_t>(v);
+}
+
+__device__ __forceinline__ uint32_t low_bits(int n) {   // the n lowest bits, 0 <= n
+  return n >= 32 ? 0xffffffffu : (1u << n) - 1;
+}
+
+// ---------------------------------------------------------------------------
+// Work list: every role walks the same segments (a CTA's tiles of one unit).
+// ---------------------------------------------------------------------------
+
+struct Request {
+  int seq, q0, n, tiles, row_tiles;
+  __device__ __forceinline__ int work(int kv_heads) const { return kv_heads * row_tiles * tiles; }
+};
+
+// A request's lengths; false if they are inconsistent (it then has no work).
+template <int R>
+__device__ __forceinline__ bool read_request(const TreeArgs& a, int b, Request& r) {
+  r.seq = a.seq[b];
+  r.q0 = a.cu[b];
+  const int q1 = a.cu[b + 1];
+  r.n = q1 - r.q0;
+  const bool ok = r.q0 >= 0 && q1 >= r.q0 && q1 <= a.total_q && r.n <= a.max_q && r.seq >= r.n &&
+                  r.seq <= a.max_seqlen &&
+                  r.seq <= static_cast<int64_t>(a.width) << a.page_log2 &&
+                  (!a.mask || r.n <= 64ll * a.mask_words);
+  r.tiles = ok ? (r.seq + kTile - 1) / kTile : 0;
+  r.row_tiles = ok ? (r.n * a.group + R - 1) / R : 0;
+  return ok;
+}
+
+// chunk[i] = tiles of the requests before thread i's; chunk[kThreads] = all.
+// Returns whether this thread met an inconsistent request.
+template <int R, int kThreads>
+__device__ bool scan_requests(const TreeArgs& a, int* chunk, int* warp_sums) {
+  const int per = (a.rows + kThreads - 1) / kThreads;
+  const int first = min(a.rows, static_cast<int>(threadIdx.x) * per);
+  const int last = min(a.rows, first + per);
+  bool bad = false;
+  int sum = 0;
+  for (int b = first; b < last; ++b) {
+    Request r;
+    bad |= !read_request<R>(a, b, r);
+    sum += r.work(a.kv_heads);
+  }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = sum;
+#pragma unroll
+  for (int off = 1; off < 32; off *= 2) {
+    const int up = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += up;
+  }
+  if (lane == 31) warp_sums[warp] = incl;
+  __syncthreads();
+  int at = incl - sum;
+  for (int w = 0; w < warp; ++w) at += warp_sums[w];
+  chunk[threadIdx.x] = at;
+  if (threadIdx.x == kThreads - 1) chunk[kThreads] = at + sum;
+  return bad;   // (the caller syncs)
+}
+
+// The request that a work item belongs to.
+template <int R, int kThreads>
+struct Finder {
+  Request r;
+  int b = -1, start = 0, stop = 0;   // request, its first item, end of its chunk
+  __device__ __forceinline__ void seek(const TreeArgs& a, const int* chunk, int w) {
+    if (b >= 0 && w < start + r.work(a.kv_heads)) return;
+    while (b >= 0 && b + 1 < stop) {   // a neighbour of the same chunk
+      start += r.work(a.kv_heads);
+      read_request<R>(a, ++b, r);
+      if (w < start + r.work(a.kv_heads)) return;
+    }
+    int lo = 0, hi = kThreads - 1;     // the last chunk that starts at or before w
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (chunk[mid] <= w) lo = mid; else hi = mid - 1;
+    }
+    const int per = (a.rows + kThreads - 1) / kThreads;
+    b = lo * per;
+    stop = min(a.rows, b + per);
+    start = chunk[lo];
+    read_request<R>(a, b, r);
+    while (w >= start + r.work(a.kv_heads)) {
+      start += r.work(a.kv_heads);
+      read_request<R>(a, ++b, r);
+    }
+  }
+};
+
+// Tiles of a CTA's range.
+__device__ __forceinline__ int tiles_per_cta(int total, int ctas) {
+  return max(kMinTiles, (total + ctas - 1) / ctas);
+}
+
+template <int R, int kThreads>
+struct Walker {
+  Finder<R, kThreads> find;
+  int w, end;
+  __device__ __forceinline__ void init(const int* chunk, int ctas) {
+    const int total = chunk[kThreads];
+    const int per = tiles_per_cta(total, ctas);
+    const int64_t from = static_cast<int64_t>(blockIdx.x) * per;
+    w = static_cast<int>(min(from, static_cast<int64_t>(total)));
+    end = static_cast<int>(min(from + per, static_cast<int64_t>(total)));
+  }
+  __device__ __forceinline__ bool next(const TreeArgs& a, const int* chunk, Segment& s) {
+    if (w >= end) return false;
+    find.seek(a, chunk, w);
+    const Request& r = find.r;
+    s.b = find.b;
+    s.seq = r.seq;
+    s.q0 = r.q0;
+    s.n = r.n;
+    s.tiles = r.tiles;
+    const int local = w - find.start;
+    const int unit = local / r.tiles;
+    s.head = unit / r.row_tiles;
+    s.rt = unit - s.head * r.row_tiles;
+    s.t0 = local - unit * r.tiles;
+    s.t1 = min(s.tiles, s.t0 + (end - w));
+    w += s.t1 - s.t0;
+    return true;
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Waits.  One that gives up sets the abort flag, which ends all other waits at
+// once; the roles then run on without data (so that every barrier is met) and
+// write no output.  (The whole warp tests: 64 cycles when the phase is over
+// already, against 117 for one lane and a warp sync.)
+// ---------------------------------------------------------------------------
+
+struct Waits {
+  int* abort_flag;       // shared memory
+  int32_t* err;
+  int lane;
+  __device__ __forceinline__ bool aborted() const {
+    return *const_cast<volatile int*>(abort_flag) != 0;
+  }
+  __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity) const {
+    if (!mbar_wait(bar, parity, const_cast<volatile int*>(abort_flag))) {
+      if (!aborted()) raise_error(err, kErrTimeout);
+      *const_cast<volatile int*>(abort_flag) = 1;
+    }
+    __syncwarp();
+  }
+  // one arrival for the warp
+  __device__ __forceinline__ void arrive(uint64_t* bar) const {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  }
+};
+
+// ---------------------------------------------------------------------------
+// TMA producer of K or of V (a warp each: neither waits for the other's
+// stages): a box per page, one lane per page, page ids looked up a tile ahead.
+// A page id outside the cache is outside the tensor map: zeros arrive.  Before
+// stage i's n-th refill (n >= 1) it waits for phase n - 1 of free1[i], and of
+// free2[i] if there is one.  After an abort the copies go on, into stages that
+// nobody reads.
+// ---------------------------------------------------------------------------
+
+template <int R, int kThreads, bool kFp8>
+__device__ __forceinline__ void produce(const TreeArgs& a, const Waits& w, const int* chunk, const CUtensorMap* map,
+                        bool report, uint8_t* ring, int stages, uint64_t* full, uint64_t* free1,
+                        uint64_t* free2) {
+  constexpr int kBytes = kFp8 ? 16384 : 32768;   // of a tile
+  const int page = 1 << a.page_log2;
+  const int box = min(page, kTile);
+  const int box_log2 = min(a.page_log2, 7);
+  Walker<R, kThreads> walk;
+  walk.init(chunk, gridDim.x);
+  Segment seg;
+  int g = 0, stage = 0, turn = 0;
+  while (!w.aborted() && walk.next(a, chunk, seg)) {
+    const int32_t* table = a.tables + seg.b * a.table_stride;
+    auto look_up = [&](int t) {
+      const int key = t * kTile + (w.lane << box_log2);
+      if (w.lane >= kTile >> box_log2 || key >= seg.seq) return -2;
+      return __ldg(table + (key >> a.page_log2));
+    };
+    int next_id = look_up(seg.t0);
+    for (int t = seg.t0; t < seg.t1; ++t, ++g) {
+      const int id = next_id;
+      if (t + 1 < seg.t1) next_id = look_up(t + 1);
+      const bool load = id != -2;
+      if (report && load && (id < 0 || id >= a.num_pages)) raise_error(a.err, kErrPages);
+      const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, load)) * box * (kFp8 ? 128 : 256);
+      const int row = a.page_log2 > 7 ? (t * kTile) & (page - 1) : 0;
+      if (turn > 0) {
+        w.wait(&free1[stage], (turn - 1) & 1);
+        if (free2) w.wait(&free2[stage], (turn - 1) & 1);
+      }
+      if (w.lane == 0) mbar_expect_tx(&full[stage], bytes);
+      __syncwarp();
+      if (load) {
+        uint8_t* dst = ring + stage * kBytes + w.lane * box * 128;
+        tma_load_4d(dst, map, &full[stage], 0, seg.head, row, id);
+        if (!kFp8) tma_load_4d(dst + 16384, map, &full[stage], 64, seg.head, row, id);
+      }
+      __syncwarp();
+      if (++stage == stages) stage = 0, ++turn;
+    }
+  }
+  // no copy may still be landing when the CTA leaves
+  if (w.lane == 0)
+    for (int i = max(0, g - stages); i < g; ++i)
+      mbar_wait(&full[i % stages], (i / stages) & 1, nullptr);
+  __syncwarp();
+}
+
+// ---------------------------------------------------------------------------
+// Q of a unit: a half warp per row, 8 channels a lane, loaded a unit ahead.
+// K-major rows of 128 bytes, 128-byte swizzle; bf16: two 64-channel halves;
+// E4M3: hi tile, then the remainders (times kLoScale) R rows on.
+// ---------------------------------------------------------------------------
+
+template <int R>
+struct QLoads {
+  static constexpr int kLoads = R * 16 / kPrepThreads, kRows = kPrepThreads / 16;
+  uint4 x[kLoads];
+  __device__ __forceinline__ void load(const TreeArgs& a, const Segment& s, int tid) {
+#pragma unroll
+    for (int it = 0; it < kLoads; ++it) {
+      const int row = s.rt * R + it * kRows + (tid >> 4);
+      const int node = row / a.group, gq = row - node * a.group;
+      x[it] = make_uint4(0, 0, 0, 0);
+      if (node < s.n)
+        x[it] = __ldg(reinterpret_cast<const uint4*>(a.q + (s.q0 + node) * a.q_tok_stride +
+                                                     (s.head * a.group + gq) * a.q_head_stride +
+                                                     (tid & 15) * 8));
+    }
+  }
+};
+
+// 2^e <= amax < 2^(e + 1) for bf16 bits; 2^(7 - e) and 2^(e - 7) are normal.
+__device__ __forceinline__ int exponent_of(uint32_t bits) {
+  return max(static_cast<int>(bits >> 7) - 127, -119);
+}
+
+__device__ __forceinline__ float power_of_two(int e) {
+  return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+}
+
+template <int R, bool kFp8, int kLoScale>
+__device__ __forceinline__ void store_q(const TreeArgs& a, const Segment& s, const QLoads<R>& q, uint8_t* sq,
+                        UnitRows<R>& rows, uint2* row_max, int barrier, float unit_factor,
+                        int tid) {
+  constexpr int kLoads = QLoads<R>::kLoads, kRows = QLoads<R>::kRows;
+  const int c = tid & 15, lane = tid & 31;
+  if constexpr (kFp8) {
+    // |x| max of this thread's rows, as bf16 bits, and the tile's extremes
+    uint32_t amax[kLoads], most = 0, least = 0xffffffffu;
+#pragma unroll
+    for (int it = 0; it < kLoads; ++it) {
+      const uint32_t w[4] = {q.x[it].x, q.x[it].y, q.x[it].z, q.x[it].w};
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+      m = max(m & 0xFFFFu, m >> 16);
+#pragma unroll
+      for (int off = 8; off >= 1; off /= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+      amax[it] = m;
+      if (m < 0x7F80u) most = max(most, m);
+      if (m != 0) least = min(least, m);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    least = __reduce_min_sync(0xffffffffu, least);
+    if (lane == 0) row_max[tid >> 5] = make_uint2(most, least);
+    group_sync(barrier, kPrepThreads);
+#pragma unroll
+    for (int i = 0; i < kPrepWarps; ++i) {
+      const uint2 m = row_max[i];
+      most = max(most, m.x);
+      least = min(least, m.y);
+    }
+    // rows within 2^4 of the largest share its scale: a factor in a register
+    // instead of one in shared memory per column; otherwise each has its own
+    // (with remainders unscaled they are too coarse for that)
+    const bool shared = kLoScale > 1 && most <= (least & 0x7F80u) + (4u << 7) + 127u;
+    if (tid == 0) rows.one_factor = shared;
+#pragma unroll
+    for (int it = 0; it < kLoads; ++it) {
+      const int r = it * kRows + (tid >> 4);
+      const uint32_t w[4] = {q.x[it].x, q.x[it].y, q.x[it].z, q.x[it].w};
+      const int e = exponent_of(shared ? most : amax[it]);
+      const float up = power_of_two(7 - e);
+      const bool whole = amax[it] < 0x7F80u;   // a row with Inf or NaN is NaN throughout
+      uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float x0 = __uint_as_float(w[i] << 16) * up;
+        const float x1 = __uint_as_float(w[i] & 0xFFFF0000u) * up;
+        const uint32_t h = cvt_e4m3x2(x0, x1);
+        const uint32_t hf = cvt_f16x2_from_e4m3x2(h);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hf));
+        const uint32_t l = cvt_e4m3x2((x0 - f.x) * kLoScale, (x1 - f.y) * kLoScale);
+        hi[i >> 1] |= (whole ? h : 0x7F7Fu) << (16 * (i & 1));
+        lo[i >> 1] |= (whole ? l : 0x7F7Fu) << (16 * (i & 1));
+      }
+      uint8_t* to = sq + (r >> 3) * 1024 + (r & 7) * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
+      *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(to + R * 128) = make_uint2(lo[0], lo[1]);
+      if (c == 0) rows.factor[r] = unit_factor * power_of_two(e - 7);
+    }
+  } else {
+#pragma unroll
+    for (int it = 0; it < kLoads; ++it) {
+      const int r = it * kRows + (tid >> 4);
+      *reinterpret_cast<uint4*>(sq + (c >> 3) * (R * 128) + (r >> 3) * 1024 + (r & 7) * 128 +
+                                (((c & 7) ^ (r & 7)) << 4)) = q.x[it];
+    }
+    if (tid < R) rows.factor[tid] = unit_factor;
+    if (tid == 0) rows.one_factor = 1;
+  }
+  if (tid < R) {
+    const int row = s.rt * R + tid;
+    const int node = row / a.group, gq = row - node * a.group;
+    const bool live = node < s.n;
+    rows.node[tid] = live ? node : -1;
+    rows.out_row[tid] = live ? (s.q0 + node) * (a.kv_heads * a.group) + s.head * a.group + gq : -1;
+  }
+  if (tid == 0) rows.seg = s;
+  fence_proxy_async();
+}
+
+// ---------------------------------------------------------------------------
+// V of a tile.  In tiles that hold nodes, rows past the sequence become zeros,
+// and so do the non-finite elements of nodes, which a query that does not see
+// the node must not meet as 0 x Inf: the epilogue adds them.  Both return
+// whether this thread met such an element; pos0 = position of the tile's first
+// key, nodes begin at position ctx.
+// ---------------------------------------------------------------------------
+
+// E4M3 -> f16 into two 64-channel halves of 128-byte rows, 128-byte swizzle.
+// A thread's pieces of 16 channels: c = tid & 7 of rows 16 i + tid / 8.  They
+// become pieces 2 (c & 3) and + 1 of half c >> 2; the halves start with
+// different ones (no bank conflicts).  `taken` runs when the source is read,
+// `ready` before the destination is written.
+template <int kBatch, class Taken, class Ready>
+__device__ __forceinline__ bool widen_v(const uint8_t* src, uint8_t* wide, int tid, bool tail,
+                                        int pos0, int ctx, int seq, Taken taken, Ready ready) {
+  bool wild = false;
+  const int row = tid >> 3, c = tid & 7, odd = c >> 2;
+  uint8_t* to = wide + odd * 16384 + row * 128;
+  const int p0 = ((2 * (c & 3) + odd) ^ (row & 7)) << 4;
+  const int p1 = ((2 * (c & 3) + (odd ^ 1)) ^ (row & 7)) << 4;
+#pragma unroll 1
+  for (int i0 = 0; i0 < 8; i0 += kBatch) {
+    uint4 x[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      x[i] = *reinterpret_cast<const uint4*>(src + ((i0 + i) * kPrepThreads + (tid ^ (row & 7))) * 16);
+    if (i0 + kBatch == 8) taken();
+    if (tail) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int pos = pos0 + (i0 + i) * 16 + row;
+        uint32_t* w = &x[i].x;
+        uint32_t nan = 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const uint32_t m = pos >= seq   ? 0xffffffffu
+                             : pos >= ctx ? __vcmpeq4(w[u] & 0x7F7F7F7Fu, 0x7F7F7F7Fu)
+                                          : 0u;
+          w[u] &= ~m;
+          nan |= m;
+        }
+        wild |= nan != 0 && pos < seq;
+      }
+    }
+    if (i0 == 0) ready();
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      uint32_t f[8];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t w = (&x[i].x)[u];
+        f[2 * u] = cvt_f16x2_from_e4m3x2(w & 0xFFFFu);
+        f[2 * u + 1] = cvt_f16x2_from_e4m3x2(w >> 16);
+      }
+      const uint4 lo = make_uint4(f[0], f[1], f[2], f[3]);
+      const uint4 hi = make_uint4(f[4], f[5], f[6], f[7]);
+      uint8_t* d = to + (i0 + i) * 2048;
+      *reinterpret_cast<uint4*>(d + p0) = odd ? hi : lo;
+      *reinterpret_cast<uint4*>(d + p1) = odd ? lo : hi;
+    }
+  }
+  fence_proxy_async();
+  return wild;
+}
+
+// A bf16 tile that holds nodes, in place.
+__device__ __forceinline__ bool mend_v(uint8_t* src, int tid, int pos0, int ctx, int seq) {
+  bool wild = false;
+  for (int i = tid; i < 32768 / 16; i += kPrepThreads) {
+    const int pos = pos0 + ((i >> 3) & 127);
+    if (pos < ctx) continue;
+    uint4* p = reinterpret_cast<uint4*>(src + i * 16);
+    uint4 x = pos < seq ? *p : make_uint4(0, 0, 0, 0);
+    uint32_t* w = &x.x;
+    uint32_t found = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t m = __vcmpeq2(w[u] & 0x7F807F80u, 0x7F807F80u);
+      w[u] &= ~m;
+      found |= m;
+    }
+    if (found || pos >= seq) *p = x;
+    wild |= found != 0;
+  }
+  fence_proxy_async();
+  return wild;
+}
+
+// A non-finite element of the V cache as fp32, 0 for a finite one.
+template <bool kFp8>
+__device__ __forceinline__ float wild_value(const uint8_t* v, int64_t at) {
+  if (kFp8) return (v[at] & 0x7Fu) == 0x7Fu ? __uint_as_float(0x7FC00000u) : 0.0f;
+  const uint32_t u = reinterpret_cast<const uint16_t*>(v)[at];
+  return (u & 0x7F80u) == 0x7F80u ? __uint_as_float(u << 16) : 0.0f;
+}
+
+// 16-byte pieces of V that a preparing thread has in flight: as many as its
+// registers hold beside the next unit's Q (16 R / 128 pieces).
+template <int R>
+constexpr int kWidenBatch = R == 16 ? 8 : 4;
+
+// The preparing warps of a CTA: hand out the units (rows[u & 3], q_full[u & 1],
+// an empty segment at the end) with their Q, and make V ready tile by tile.
+// s_done(g) waits until tile g's scores are done (Q's place is then free),
+// o_done(g) until its product is (the widened V's place).
+template <int R, int kThreads, bool kFp8, int kLoScale, int kVStages, int kWideRing, class SDone,
+          class ODone>
+__device__ __forceinline__ void prepare(const TreeArgs& a, const Waits& w, const int* chunk, uint8_t* sq,
+                        uint8_t* sv, uint8_t* swide, UnitRows<R>* rows, uint2* row_max,
+                        int barrier, uint64_t* q_full, uint64_t* v_full, uint64_t* v_empty,
+                        uint64_t* wide_full, int* flagged, int tid, SDone s_done, ODone o_done) {
+  const float unit_factor = a.softmax_scale * kLog2e * (kFp8 ? __ldg(a.descale + 1) : 1.0f);
+  Walker<R, kThreads> walk;
+  walk.init(chunk, gridDim.x);
+  Segment seg, next;
+  QLoads<R> q;
+  bool more = walk.next(a, chunk, next);
+  if (more) q.load(a, next, tid);
+  int g = 0, tails = 0;
+  for (int unit = 0;; ++unit) {
+    seg = next;
+    if (g > 0) s_done(g - 1);
+    if (more)
+      store_q<R, kFp8, kLoScale>(a, seg, q, sq, rows[unit & 3], row_max, barrier, unit_factor, tid);
+    else if (tid == 0)
+      rows[unit & 3].seg.t0 = rows[unit & 3].seg.t1 = 0;
+    w.arrive(&q_full[unit & 1]);
+    if (!more) return;
+    more = walk.next(a, chunk, next);
+    if (more) q.load(a, next, tid);
+    const int ctx = seg.seq - seg.n;
+    for (int t = seg.t0; t < seg.t1; ++t, ++g) {
+      const bool tail = t * kTile + kTile > ctx;
+      const int vs = g % kVStages;
+      bool wild = false;
+      w.wait(&v_full[vs], (g / kVStages) & 1);
+      if constexpr (kFp8) {
+        wild = widen_v<kWidenBatch<R>>(
+            sv + vs * 16384, swide + (g % kWideRing) * 32768, tid, tail, t * kTile, ctx, seg.seq,
+            [&]() { w.arrive(&v_empty[vs]); },
+            [&]() { if (g >= kWideRing) o_done(g - kWideRing); });
+      } else if (tail) {
+        wild = mend_v(sv + vs * 32768, tid, t * kTile, ctx, seg.seq);
+      }
+      if (wild) *const_cast<volatile int*>(&flagged[(unit + 1) & 3]) = unit + 1;
+      if (kFp8 || tail) {
+        const int i = kFp8 ? g : tails++;
+        w.arrive(&wide_full[i % kWideRing]);
+      }
+      if (!kFp8) w.arrive(&v_empty[vs]);   // (the stage's next phase may begin)
+    }
+  }
+}
+
+}  // namespace kv_tree
+
+}  // namespace fp8attn

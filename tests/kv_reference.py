@@ -67,7 +67,9 @@ def tree_attention(q, k_cache, v_cache, tables, seq, cu, mask=None, scale=None, 
       - score: fp32 accumulation of 128 products, at most 16 u sum |q k| (the
         bound the library's score self-test checks), four more roundings of
         the score and of the reference it is taken against, and, for an E4M3
-        cache, Q represented to 2^-22 of its row's largest element;
+        cache, Q represented to 2^-17 of its row's largest element (a row is
+        scaled to a largest element of 2^3 at least with remainders rounded to
+        2^-14, or of 2^7 at least with remainders rounded to 2^-10);
       - a weight w_j moves by the score's error (twice: its own and the
         maximum's), by P's rounding, by the exponential's 2^-21;
       - P V: fp32 accumulation over the key tiles;
@@ -108,7 +110,7 @@ def tree_attention(q, k_cache, v_cache, tables, seq, cu, mask=None, scale=None, 
                     ds_score = 16 * U32 * (np.abs(kk) @ np.abs(qi)) * scale + \
                         4 * U32 * (np.abs(s) + np.abs(s).max())
                     if fp8:
-                        ds_score = ds_score + 2.0 ** -22 * np.abs(qi).max() * \
+                        ds_score = ds_score + 2.0 ** -17 * np.abs(qi).max() * \
                             np.abs(kk).sum(1) * scale
                     per_weight = 2 * ds_score.max() + (HALF_F16 if fp8 else HALF_BF16) + 2.0 ** -20 + \
                         (16 + L / 128) * U32
