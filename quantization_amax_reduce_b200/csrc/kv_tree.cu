@@ -175,9 +175,10 @@ kv_tree_keys_kernel(const __grid_constant__ CUtensorMap tm_k,
   const uint32_t tmem = ctl.tmem_base;
   const Waits w{&ctl.abort_flag, a.err, lane};
   auto wait_pv = [&](int g) { w.wait(&ctl.pv_done[g % C::kPvRing], (g / C::kPvRing) & 1); };
-  auto unit_at = [&](int unit, Segment& s) {
+  // whether there is such a unit; the preparing warps have handed it out then
+  auto unit_at = [&](int unit) {
     w.wait(&ctl.q_full[unit & 1], (unit >> 1) & 1);
-    s = ctl.rows[unit & 3].seg;
+    const Segment& s = ctl.rows[unit & 3].seg;
     return s.t0 < s.t1 && !w.aborted();
   };
 
@@ -249,8 +250,8 @@ kv_tree_keys_kernel(const __grid_constant__ CUtensorMap tm_k,
       if (++vs == C::kPvRing) vs = 0, v_turn ^= 1;
     };
     for (int unit = 0;; ++unit) {
-      Segment seg;
-      const bool go = unit_at(unit, seg);
+      const bool go = unit_at(unit);
+      const Segment& seg = ctl.rows[unit & 3].seg;
       if (!__shfl_sync(0xffffffffu, static_cast<int>(go), 0)) break;
       const int n = __shfl_sync(0xffffffffu, seg.t1 - seg.t0, 0);
       // tiles from this one on hold nodes
@@ -289,10 +290,13 @@ kv_tree_keys_kernel(const __grid_constant__ CUtensorMap tm_k,
     uint8_t* prow = sp + key * C::kPitch;
     const int pswz = R == 32 ? (key >> 1) & 3 : (key >> 2) & 1;
     const float ds_v = kFp8 ? __ldg(a.descale + 2) : 1.0f;
-    Segment seg;
+    if (threadIdx.x == 0 && a.join) a.join[blockIdx.x] = {0, 0, 0, 0, 0};
     int g = 0;
-    for (int unit = 0; unit_at(unit, seg); ++unit) {
+    for (int unit = 0; unit_at(unit); ++unit) {
       const UnitRows<R>& col = ctl.rows[unit & 3];
+      const Segment& seg = col.seg;   // (in shared memory: registers are short)
+      if (threadIdx.x == 0 && seg.t0 == 0 && seg.t1 < seg.tiles)
+        a.join[blockIdx.x] = join_info(seg, tiles_per_cta(ctl.chunk[C::kThreads], gridDim.x));
       const int ctx = seg.seq - seg.n;
       // columns in pairs: row sums of this thread's keys; kPOffset - ref, 0 while unset
       uint64_t sum2[kCols / 2], off2[kCols / 2];
@@ -629,9 +633,10 @@ kv_tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
   const uint32_t tmem = ctl.tmem_base;
   const Waits w{&ctl.abort_flag, a.err, lane};
   auto wait_pv = [&](int g) { w.wait(&ctl.pv_done[g & 1], (g >> 1) & 1); };
-  auto unit_at = [&](int unit, Segment& s) {
+  // whether there is such a unit; the preparing warps have handed it out then
+  auto unit_at = [&](int unit) {
     w.wait(&ctl.q_full[unit & 1], (unit >> 1) & 1);
-    s = ctl.rows[unit & 3].seg;
+    const Segment& s = ctl.rows[unit & 3].seg;
     return s.t0 < s.t1 && !w.aborted();
   };
 
@@ -699,8 +704,8 @@ kv_tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
       if (side == 0) turn ^= 1;
     };
     for (int unit = 0;; ++unit) {
-      Segment seg;
-      const bool go = unit_at(unit, seg);
+      const bool go = unit_at(unit);
+      const Segment& seg = ctl.rows[unit & 3].seg;
       if (!__shfl_sync(0xffffffffu, static_cast<int>(go), 0)) break;
       const int n = __shfl_sync(0xffffffffu, seg.t1 - seg.t0, 0);
       const int tail0 = __shfl_sync(0xffffffffu, (seg.seq - seg.n) / kTile - seg.t0, 0);
@@ -729,10 +734,13 @@ kv_tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
     const uint32_t t_s = tmem + lane_off + 128 * wg;
     const uint32_t t_o = tmem + lane_off + C::kO + 128 * wg;
     const float ds_v = kFp8 ? __ldg(a.descale + 2) : 1.0f;
-    Segment seg;
+    if (threadIdx.x == 0 && a.join) a.join[blockIdx.x] = {0, 0, 0, 0, 0};
     int g = 0;
-    for (int unit = 0; unit_at(unit, seg); ++unit) {
+    for (int unit = 0; unit_at(unit); ++unit) {
       const UnitRows<R>& rows = ctl.rows[unit & 3];
+      const Segment& seg = rows.seg;   // (in shared memory: registers are short)
+      if (threadIdx.x == 0 && seg.t0 == 0 && seg.t1 < seg.tiles)
+        a.join[blockIdx.x] = join_info(seg, tiles_per_cta(ctl.chunk[C::kThreads], gridDim.x));
       const int ctx = seg.seq - seg.n;
       const float factor = rows.factor[row];
       const int node = rows.node[row];
@@ -915,58 +923,35 @@ kv_tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
 }
 
 // ---------------------------------------------------------------------------
-// Join: block (x, y) takes the unit that crosses from CTA x's range into CTA
-// x + 1's, if it starts in CTA x's, and rows 8 y .. 8 y + 7 of it:
+// Join: block (x, y) takes the unit that begins in CTA x's range and leaves it,
+// and rows kJoinRows y .. of it, a warp per row, four channels a lane:
 // out = sum_i 2^(ref_i - ref) O_i ds_v / sum_i 2^(ref_i - ref) l_i, pieces in
 // order.  Bound: launch and latency; the pieces are in L2.
 // ---------------------------------------------------------------------------
 
 constexpr int kJoinThreads = 256;
-constexpr int kJoinRows = kJoinThreads / 32;
+constexpr int kJoinRows = 16;
 
 template <int R, bool kFp8>
-__global__ void __launch_bounds__(kJoinThreads) kv_tree_join_kernel(const TreeArgs a, int ctas) {
-  __shared__ int chunk[kJoinThreads + 1];
-  __shared__ int warp_sums[kJoinThreads / 32];
-  __shared__ float s_scale[kJoinRows][kMaxCtas];
-  // everything up to the wait needs the lengths alone
-  scan_requests<R, kJoinThreads>(a, chunk, warp_sums);
-  __syncthreads();
-  const int total = chunk[kJoinThreads];
-  const int per = tiles_per_cta(total, ctas);
-  const int64_t border = static_cast<int64_t>(blockIdx.x + 1) * per;
-  Finder<R, kJoinThreads> find;
-  const Request& q = find.r;
-  const int w = static_cast<int>(min(border, static_cast<int64_t>(total)));
-  int unit = 0, c0 = -1, c1 = -1;     // the unit at the border, and its CTAs
-  if (w < total) {
-    find.seek(a, chunk, w);
-    unit = (w - find.start) / q.tiles;
-    const int from = find.start + unit * q.tiles;
-    if (from < w) {
-      c0 = from / per;
-      c1 = (from + q.tiles - 1) / per;
-    }
-  }
+__global__ void __launch_bounds__(kJoinThreads) kv_tree_join_kernel(const TreeArgs a) {
+  __shared__ float s_scale[kJoinThreads / 32][kMaxCtas];
+  const float ds_v = kFp8 ? __ldg(a.descale + 2) : 1.0f;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (c0 != static_cast<int>(blockIdx.x)) return;   // none, or an earlier border's
-  const int head = unit / q.row_tiles, rt = unit - head * q.row_tiles;
+  const JoinInfo u = a.join[blockIdx.x];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int pieces = c1 - c0 + 1;
-  // piece i of row r; the first CTA's piece is its last one, the others' their first
-  auto at = [&](int i, int r) {
-    return (2 * static_cast<int64_t>(c0 + i) + (i == 0)) * R + blockIdx.y * kJoinRows + r;
-  };
-  // a warp per row: the pieces' weights
-  float inv;
-  {
-    float m = -INFINITY;
-    for (int i = lane; i < pieces; i += 32) m = fmaxf(m, a.part_ml[at(i, warp)].x);
+  for (int i0 = warp; i0 < kJoinRows; i0 += kJoinThreads / 32) {
+    const int r = blockIdx.y * kJoinRows + i0;
+    const int row = u.rt * R + r;
+    const int node = row / a.group;
+    if (u.pieces == 0 || node >= u.n) return;
+    // piece i; the first CTA's piece is its last one, the others' their first
+    auto at = [&](int i) { return (2 * static_cast<int64_t>(blockIdx.x + i) + (i == 0)) * R + r; };
+    float m = -INFINITY, l = 0.0f;
+    for (int i = lane; i < u.pieces; i += 32) m = fmaxf(m, a.part_ml[at(i)].x);
 #pragma unroll
     for (int off = 16; off >= 1; off /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    float l = 0.0f;
-    for (int i = lane; i < pieces; i += 32) {
-      const float2 ml = a.part_ml[at(i, warp)];
+    for (int i = lane; i < u.pieces; i += 32) {
+      const float2 ml = a.part_ml[at(i)];
       // a piece of no visible key has ref = -inf, O = 0 and l = 0; one whose
       // scores were all NaN has ref = -inf and l = NaN
       const float scale = ml.x == -INFINITY ? 1.0f : exp2f(ml.x - m);
@@ -975,27 +960,25 @@ __global__ void __launch_bounds__(kJoinThreads) kv_tree_join_kernel(const TreeAr
     }
 #pragma unroll
     for (int off = 16; off >= 1; off /= 2) l += __shfl_xor_sync(0xffffffffu, l, off);
-    inv = l == 0.0f ? 0.0f : (kFp8 ? __ldg(a.descale + 2) : 1.0f) / l;
-  }
-  __syncwarp();
-  const int row = rt * R + blockIdx.y * kJoinRows + warp;
-  const int node = row / a.group;
-  if (node >= q.n) return;
-  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const float inv = l == 0.0f ? 0.0f : ds_v / l;
+    __syncwarp();
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
-  for (int i = 0; i < pieces; ++i) {
-    const float s = s_scale[warp][i];
-    const float4 x = *reinterpret_cast<const float4*>(a.part_o + at(i, warp) * kHeadDim + 4 * lane);
-    o.x = fmaf(s, x.x, o.x);
-    o.y = fmaf(s, x.y, o.y);
-    o.z = fmaf(s, x.z, o.z);
-    o.w = fmaf(s, x.w, o.w);
+    for (int i = 0; i < u.pieces; ++i) {
+      const float s = s_scale[warp][i];
+      const float4 x = *reinterpret_cast<const float4*>(a.part_o + at(i) * kHeadDim + 4 * lane);
+      o.x = fmaf(s, x.x, o.x);
+      o.y = fmaf(s, x.y, o.y);
+      o.z = fmaf(s, x.z, o.z);
+      o.w = fmaf(s, x.w, o.w);
+    }
+    __syncwarp();
+    if (inv == 0.0f) o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const int64_t out_row = static_cast<int64_t>(u.q0 + node) * (a.kv_heads * a.group) +
+                            u.head * a.group + (row - node * a.group);
+    *reinterpret_cast<uint2*>(a.out + out_row * kHeadDim + 4 * lane) =
+        make_uint2(cvt_bf16x2(o.x * inv, o.y * inv), cvt_bf16x2(o.z * inv, o.w * inv));
   }
-  const int64_t out_row = static_cast<int64_t>(q.q0 + node) * (a.kv_heads * a.group) +
-                          head * a.group + (row - node * a.group);
-  if (inv == 0.0f) o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  *reinterpret_cast<uint2*>(a.out + out_row * kHeadDim + 4 * lane) =
-      make_uint2(cvt_bf16x2(o.x * inv, o.y * inv), cvt_bf16x2(o.z * inv, o.w * inv));
 }
 
 // ---------------------------------------------------------------------------
@@ -1101,7 +1084,7 @@ cudaError_t launch_t(const KvTreeLaunch& p, const TreeArgs& a, cudaStream_t stre
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_tree_join_kernel<R, kFp8>, a, ctas);
+  return cudaLaunchKernelEx(&cfg, kv_tree_join_kernel<R, kFp8>, a);
 }
 
 }  // namespace
@@ -1116,7 +1099,8 @@ size_t kv_tree_workspace_bytes(int rows, int max_q, int max_seqlen, int heads, i
   const int ctas = launch_ctas(rows, max_q, max_seqlen, heads, kv_heads);
   if (ctas <= 1) return 0;
   return static_cast<size_t>(2 * ctas) * tile_rows(max_q, heads, kv_heads) *
-         (kHeadDim * sizeof(float) + sizeof(float2));
+             (kHeadDim * sizeof(float) + sizeof(float2)) +
+         ctas * sizeof(JoinInfo);
 }
 
 cudaError_t launch_kv_tree(const KvTreeLaunch& p, cudaStream_t stream) {
@@ -1151,6 +1135,8 @@ cudaError_t launch_kv_tree(const KvTreeLaunch& p, cudaStream_t stream) {
   const int ctas = launch_ctas(p.rows, p.max_q, p.max_seqlen, p.heads, p.cache.heads);
   a.part_o = static_cast<float*>(p.workspace);
   a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<size_t>(2 * ctas) * R * kHeadDim);
+  a.join = ctas > 1 ? reinterpret_cast<JoinInfo*>(a.part_ml + static_cast<size_t>(2 * ctas) * R)
+                    : nullptr;
   if (p.cache.fp8)
     return R == 16   ? launch_t<16, true>(p, a, stream)
            : R == 32 ? launch_t<32, true>(p, a, stream)

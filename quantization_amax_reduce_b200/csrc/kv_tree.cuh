@@ -46,6 +46,7 @@ struct TreeArgs {
   __nv_bfloat16* out;
   float* part_o;                         // [2 CTAs][R][128]
   float2* part_ml;                       // [2 CTAs][R] {ref, sum}
+  struct JoinInfo* join;                 // [CTAs] the unit that begins in a CTA and leaves it
   int32_t* err;
 };
 
@@ -54,6 +55,12 @@ struct Segment {
   int b, head, rt;       // request, KV head, row tile
   int seq, q0, n;
   int tiles, t0, t1;     // tiles of the unit; this CTA's (none: the end)
+};
+
+// A unit of several pieces: they lie in this CTA and the next ones (none: no
+// such unit).
+struct JoinInfo {
+  int q0, n, head, rt, pieces;
 };
 
 // What a unit's rows stand for.  Units u and u + 1 may be in use while unit
@@ -198,7 +205,11 @@ __device__ bool scan_requests(const TreeArgs& a, int* chunk, int* warp_sums) {
   if (lane == 31) warp_sums[warp] = incl;
   __syncthreads();
   int at = incl - sum;
-  for (int w = 0; w < warp; ++w) at += warp_sums[w];
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    const int s = warp_sums[w];
+    at += w < warp ? s : 0;
+  }
   chunk[threadIdx.x] = at;
   if (threadIdx.x == kThreads - 1) chunk[kThreads] = at + sum;
   return bad;   // (the caller syncs)
@@ -209,6 +220,7 @@ template <int R, int kThreads>
 struct Finder {
   Request r;
   int b = -1, start = 0, stop = 0;   // request, its first item, end of its chunk
+  // (the whole warp)
   __device__ __forceinline__ void seek(const TreeArgs& a, const int* chunk, int w) {
     if (b >= 0 && w < start + r.work(a.kv_heads)) return;
     while (b >= 0 && b + 1 < stop) {   // a neighbour of the same chunk
@@ -216,11 +228,15 @@ struct Finder {
       read_request<R>(a, ++b, r);
       if (w < start + r.work(a.kv_heads)) return;
     }
-    int lo = 0, hi = kThreads - 1;     // the last chunk that starts at or before w
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (chunk[mid] <= w) lo = mid; else hi = mid - 1;
-    }
+    // the last chunk that starts at or before w: 32 lanes probe every kStep-th,
+    // then the ones after the last that does
+    constexpr int kStep = (kThreads + 31) / 32;
+    const int lane = threadIdx.x & 31;
+    int lo = lane * kStep;
+    lo = kStep * (__popc(__ballot_sync(0xffffffffu, lo < kThreads && chunk[min(lo, kThreads)] <= w)) - 1);
+    const int probe = lo + lane;
+    lo += __popc(__ballot_sync(0xffffffffu, lane < kStep && probe < kThreads &&
+                                                chunk[min(probe, kThreads)] <= w)) - 1;
     const int per = (a.rows + kThreads - 1) / kThreads;
     b = lo * per;
     stop = min(a.rows, b + per);
@@ -236,6 +252,11 @@ struct Finder {
 // Tiles of a CTA's range.
 __device__ __forceinline__ int tiles_per_cta(int total, int ctas) {
   return max(kMinTiles, (total + ctas - 1) / ctas);
+}
+
+// The pieces of a unit that begins with `s`, which its CTA does not finish.
+__device__ __forceinline__ JoinInfo join_info(const Segment& s, int per) {
+  return {s.q0, s.n, s.head, s.rt, 1 + (s.tiles - s.t1 + per - 1) / per};
 }
 
 template <int R, int kThreads>

@@ -100,7 +100,7 @@ def test_tree_workspace(L):
         assert f(*bad) == 0
     # grows with each bound, and stops at a CTA per SM
     assert f(1, 1, 128, 8, 8) <= f(1, 1, 1 << 20, 8, 8) <= f(8, 1, 1 << 20, 8, 8)
-    assert f(8, 1, 1 << 20, 8, 8) <= f(8, 64, 1 << 20, 8, 8) <= 2 * 148 * 64 * (128 * 4 + 8)
+    assert f(8, 1, 1 << 20, 8, 8) <= f(8, 64, 1 << 20, 8, 8) <= 2 * 148 * 128 * (128 * 4 + 8) + 148 * 20
 
 
 def test_keep_path_refusals(L):
