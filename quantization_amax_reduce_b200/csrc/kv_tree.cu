@@ -77,7 +77,6 @@ using namespace kv_tree;
 // one with deep rings reads 6.4 (16 columns, E4M3).
 template <int R, bool kFp8>
 struct KeysCfg {
-  static constexpr int kRows = R;
   static constexpr int kGroups = 2;
   static constexpr int kCols = R / kGroups;               // columns of a softmax thread
   static constexpr int kSoftmaxWarps = 4 * kGroups, kSoftmaxThreads = 128 * kGroups;
@@ -538,13 +537,14 @@ kv_tree_keys_kernel(const __grid_constant__ CUtensorMap tm_k,
 // O, reference and sum, so that one's exponentials run beside the other's
 // products; they are joined like two pieces when the unit ends.  P lies in
 // TMEM over the first half of its scores, and feeds the product from there.
+// (The loops over 32 columns stay rolled: a CTA runs a unit's code once or
+// twice, and unrolled it waits for its instructions.)
 // Bound: the tensor pipe (16 products of 128 x 128 x 32 bytes a tile) and the
 // exponentials (16384 a tile at 16 a cycle).
 // ---------------------------------------------------------------------------
 
 template <bool kFp8>
 struct RowsCfg {
-  static constexpr int kRows = 128;
   static constexpr int kSoftmaxWarps = 8, kSoftmaxThreads = 256;
   static constexpr int kTmaWarp = kSoftmaxWarps, kMmaWarp = kTmaWarp + 2;   // K, V; products
   static constexpr int kPrepWarp = kMmaWarp + 1;
@@ -767,7 +767,7 @@ kv_tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
         // ---- the tile's maximum (the scores are read again below: 128 of
         // them and their exponentials do not fit the registers)
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
+#pragma unroll 1
         for (int h = 0; h < 4; ++h) {
           uint32_t u[32];
           tmem_ld32(t_s + 32 * h, u);
@@ -794,7 +794,7 @@ kv_tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
           sum2[0] = f2_mul(sum2[0], s2);
           sum2[1] = f2_mul(sum2[1], s2);
           if (rescale) {   // (O is complete: these scores were issued after its last product)
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < 4; ++h) {
               uint32_t o[32];
               tmem_ld32(t_o + 32 * h, o);
@@ -808,7 +808,7 @@ kv_tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
         }
         // ---- P: 32 scores become 16 words over scores that were read already
         const uint64_t f2 = f2_pack(factor, factor), o2 = f2_pack(off, off);
-#pragma unroll
+#pragma unroll 1
         for (int h = 0; h < 4; ++h) {
           uint32_t u[32], p[16];
           tmem_ld32(t_s + 32 * h, u);
@@ -864,7 +864,7 @@ kv_tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
       const int out_row = rows.out_row[row];
       const int64_t piece = (2 * static_cast<int64_t>(blockIdx.x) + (seg.t0 == 0)) * R + row;
       const bool live = out_row >= 0 && !w.aborted();
-#pragma unroll
+#pragma unroll 1
       for (int h = 0; h < 2; ++h) {
         const int d0 = 64 * wg + 32 * h;
         float o[32];

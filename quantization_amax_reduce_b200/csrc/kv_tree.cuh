@@ -68,7 +68,7 @@ struct JoinInfo {
 template <int R>
 struct UnitRows {
   alignas(16) float factor[R];           // score -> log2 units
-  int one_factor;                        // they are all the same
+  int one_factor;                        // they are all the same (up to 32 rows)
   int out_row[R];                        // row of `out`, -1 = none
   int node[R];                           // -1 = none
   Segment seg;
@@ -377,19 +377,21 @@ __device__ __forceinline__ void produce(const TreeArgs& a, const Waits& w, const
 }
 
 // ---------------------------------------------------------------------------
-// Q of a unit: a half warp per row, 8 channels a lane, loaded a unit ahead.
-// K-major rows of 128 bytes, 128-byte swizzle; bf16: two 64-channel halves;
-// E4M3: hi tile, then the remainders (times kLoScale) R rows on.
+// Q of a unit: a half warp per row, 8 channels a lane, four rows of a half warp
+// at a time, the first four loaded a unit ahead.  K-major rows of 128 bytes,
+// 128-byte swizzle; bf16: two 64-channel halves; E4M3: hi tile, then the
+// remainders (times kLoScale) R rows on.
 // ---------------------------------------------------------------------------
 
 template <int R>
 struct QLoads {
-  static constexpr int kLoads = R * 16 / kPrepThreads, kRows = kPrepThreads / 16;
+  static constexpr int kRows = kPrepThreads / 16;           // rows of one load
+  static constexpr int kAll = R / kRows, kLoads = kAll < 4 ? kAll : 4;
   uint4 x[kLoads];
-  __device__ __forceinline__ void load(const TreeArgs& a, const Segment& s, int tid) {
+  __device__ __forceinline__ void load(const TreeArgs& a, const Segment& s, int tid, int first) {
 #pragma unroll
     for (int it = 0; it < kLoads; ++it) {
-      const int row = s.rt * R + it * kRows + (tid >> 4);
+      const int row = s.rt * R + (first + it) * kRows + (tid >> 4);
       const int node = row / a.group, gq = row - node * a.group;
       x[it] = make_uint4(0, 0, 0, 0);
       if (node < s.n)
@@ -409,24 +411,52 @@ __device__ __forceinline__ float power_of_two(int e) {
   return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 }
 
+// |x| max of a row's 128 channels, as bf16 bits.
+__device__ __forceinline__ uint32_t row_amax(uint4 x) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+  m = max(m & 0xFFFFu, m >> 16);
+#pragma unroll
+  for (int off = 8; off >= 1; off /= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+  return m;
+}
+
+// 8 channels of row r, scaled by 2^(7 - e), as two E4M3 numbers each.
+template <int R, int kLoScale>
+__device__ __forceinline__ void split_q(uint4 x, int e, bool whole, uint8_t* sq, int r, int c) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  const float up = power_of_two(7 - e);
+  uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float x0 = __uint_as_float(w[i] << 16) * up;
+    const float x1 = __uint_as_float(w[i] & 0xFFFF0000u) * up;
+    const uint32_t h = cvt_e4m3x2(x0, x1);
+    const uint32_t hf = cvt_f16x2_from_e4m3x2(h);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hf));
+    const uint32_t l = cvt_e4m3x2((x0 - f.x) * kLoScale, (x1 - f.y) * kLoScale);
+    hi[i >> 1] |= (whole ? h : 0x7F7Fu) << (16 * (i & 1));
+    lo[i >> 1] |= (whole ? l : 0x7F7Fu) << (16 * (i & 1));
+  }
+  uint8_t* to = sq + (r >> 3) * 1024 + (r & 7) * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
+  *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
+  *reinterpret_cast<uint2*>(to + R * 128) = make_uint2(lo[0], lo[1]);
+}
+
 template <int R, bool kFp8, int kLoScale>
-__device__ __forceinline__ void store_q(const TreeArgs& a, const Segment& s, const QLoads<R>& q, uint8_t* sq,
-                        UnitRows<R>& rows, uint2* row_max, int barrier, float unit_factor,
-                        int tid) {
-  constexpr int kLoads = QLoads<R>::kLoads, kRows = QLoads<R>::kRows;
+__device__ __forceinline__ void store_q(const TreeArgs& a, const Segment& s, QLoads<R>& q,
+                                        uint8_t* sq, UnitRows<R>& rows, uint2* row_max,
+                                        int barrier, float unit_factor, int tid) {
+  constexpr int kLoads = QLoads<R>::kLoads, kRows = QLoads<R>::kRows, kAll = QLoads<R>::kAll;
   const int c = tid & 15, lane = tid & 31;
-  if constexpr (kFp8) {
-    // |x| max of this thread's rows, as bf16 bits, and the tile's extremes
+  // a row with Inf or NaN becomes NaN throughout (E4M3)
+  if constexpr (kFp8 && kAll == kLoads) {
     uint32_t amax[kLoads], most = 0, least = 0xffffffffu;
 #pragma unroll
     for (int it = 0; it < kLoads; ++it) {
-      const uint32_t w[4] = {q.x[it].x, q.x[it].y, q.x[it].z, q.x[it].w};
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
-      m = max(m & 0xFFFFu, m >> 16);
-#pragma unroll
-      for (int off = 8; off >= 1; off /= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+      const uint32_t m = row_amax(q.x[it]);
       amax[it] = m;
       if (m < 0x7F80u) most = max(most, m);
       if (m != 0) least = min(least, m);
@@ -443,42 +473,37 @@ __device__ __forceinline__ void store_q(const TreeArgs& a, const Segment& s, con
     }
     // rows within 2^4 of the largest share its scale: a factor in a register
     // instead of one in shared memory per column; otherwise each has its own
-    // (with remainders unscaled they are too coarse for that)
-    const bool shared = kLoScale > 1 && most <= (least & 0x7F80u) + (4u << 7) + 127u;
+    const bool shared = most <= (least & 0x7F80u) + (4u << 7) + 127u;
     if (tid == 0) rows.one_factor = shared;
 #pragma unroll
     for (int it = 0; it < kLoads; ++it) {
       const int r = it * kRows + (tid >> 4);
-      const uint32_t w[4] = {q.x[it].x, q.x[it].y, q.x[it].z, q.x[it].w};
       const int e = exponent_of(shared ? most : amax[it]);
-      const float up = power_of_two(7 - e);
-      const bool whole = amax[it] < 0x7F80u;   // a row with Inf or NaN is NaN throughout
-      uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float x0 = __uint_as_float(w[i] << 16) * up;
-        const float x1 = __uint_as_float(w[i] & 0xFFFF0000u) * up;
-        const uint32_t h = cvt_e4m3x2(x0, x1);
-        const uint32_t hf = cvt_f16x2_from_e4m3x2(h);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hf));
-        const uint32_t l = cvt_e4m3x2((x0 - f.x) * kLoScale, (x1 - f.y) * kLoScale);
-        hi[i >> 1] |= (whole ? h : 0x7F7Fu) << (16 * (i & 1));
-        lo[i >> 1] |= (whole ? l : 0x7F7Fu) << (16 * (i & 1));
-      }
-      uint8_t* to = sq + (r >> 3) * 1024 + (r & 7) * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
-      *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
-      *reinterpret_cast<uint2*>(to + R * 128) = make_uint2(lo[0], lo[1]);
+      split_q<R, kLoScale>(q.x[it], e, amax[it] < 0x7F80u, sq, r, c);
       if (c == 0) rows.factor[r] = unit_factor * power_of_two(e - 7);
     }
   } else {
+    // (rolled, the next rows on their way while these are stored)
+#pragma unroll 1
+    for (int first = 0; first < kAll; first += kLoads) {
+      QLoads<R> now = q;
+      if (first + kLoads < kAll) q.load(a, s, tid, first + kLoads);
 #pragma unroll
-    for (int it = 0; it < kLoads; ++it) {
-      const int r = it * kRows + (tid >> 4);
-      *reinterpret_cast<uint4*>(sq + (c >> 3) * (R * 128) + (r >> 3) * 1024 + (r & 7) * 128 +
-                                (((c & 7) ^ (r & 7)) << 4)) = q.x[it];
+      for (int it = 0; it < kLoads; ++it) {
+        const int r = (first + it) * kRows + (tid >> 4);
+        if constexpr (kFp8) {
+          const uint32_t m = row_amax(now.x[it]);
+          const int e = exponent_of(m);
+          split_q<R, kLoScale>(now.x[it], e, m < 0x7F80u, sq, r, c);
+          if (c == 0) rows.factor[r] = unit_factor * power_of_two(e - 7);
+        } else {
+          *reinterpret_cast<uint4*>(sq + (c >> 3) * (R * 128) + (r >> 3) * 1024 + (r & 7) * 128 +
+                                    (((c & 7) ^ (r & 7)) << 4)) = now.x[it];
+        }
+      }
     }
-    if (tid < R) rows.factor[tid] = unit_factor;
-    if (tid == 0) rows.one_factor = 1;
+    if (!kFp8 && tid < R) rows.factor[tid] = unit_factor;
+    if (!kFp8 && tid == 0) rows.one_factor = 1;
   }
   if (tid < R) {
     const int row = s.rt * R + tid;
@@ -609,7 +634,7 @@ __device__ __forceinline__ void prepare(const TreeArgs& a, const Waits& w, const
   Segment seg, next;
   QLoads<R> q;
   bool more = walk.next(a, chunk, next);
-  if (more) q.load(a, next, tid);
+  if (more) q.load(a, next, tid, 0);
   int g = 0, tails = 0;
   for (int unit = 0;; ++unit) {
     seg = next;
@@ -621,7 +646,7 @@ __device__ __forceinline__ void prepare(const TreeArgs& a, const Waits& w, const
     w.arrive(&q_full[unit & 1]);
     if (!more) return;
     more = walk.next(a, chunk, next);
-    if (more) q.load(a, next, tid);
+    if (more) q.load(a, next, tid, 0);
     const int ctx = seg.seq - seg.n;
     for (int t = seg.t0; t < seg.t1; ++t, ++g) {
       const bool tail = t * kTile + kTile > ctx;
