@@ -796,7 +796,7 @@ fp8attn_status fp8attn_kv_tree_fwd(const void* q, int64_t q_tok_stride, int64_t 
   if (q_tok_stride <= 0 || q_head_stride <= 0 || (q_tok_stride % 8) || (q_head_stride % 8) ||
       !aligned(q, 16) || !aligned(out, 16) || !aligned(d_tree_mask, 8) ||
       total_q > 0x7FFFFFFFLL / num_heads ||
-      static_cast<int64_t>(max_q_len) * (num_heads / num_kv_heads) > 0x7FFFFFFFLL)
+      (num_heads / num_kv_heads) > 1024)
     return FP8ATTN_ERR_UNSUPPORTED;
   // no request has more queries than there are, nor tokens than its table holds
   if (max_q_len > total_q) max_q_len = static_cast<int>(total_q);
@@ -806,6 +806,11 @@ fp8attn_status fp8attn_kv_tree_fwd(const void* q, int64_t q_tok_stride, int64_t 
       max_q_len && max_seqlen
           ? kv_tree_workspace_bytes(rows, max_q_len, max_seqlen, num_heads, num_kv_heads)
           : 0;
+  // query rows of a KV head are divided by the group in 32 bits
+  const int64_t group = num_heads / num_kv_heads;
+  if ((static_cast<int64_t>(max_q_len) * group + 128) * group > 0xFFFFFFFFLL ||
+      static_cast<int64_t>(max_q_len) * group > 0x7FFFFF00LL)
+    return FP8ATTN_ERR_UNSUPPORTED;
   if (kv_tree_max_tiles(rows, max_q_len, max_seqlen, num_heads, num_kv_heads) > 0x7FFFFFFFLL)
     return FP8ATTN_ERR_UNSUPPORTED;
   if (need > workspace_bytes || (need && !workspace)) return FP8ATTN_ERR_INVALID;

@@ -225,7 +225,7 @@ kv_tree_keys_kernel(const __grid_constant__ CUtensorMap tm_k,
       s_buf ^= 1;
       if (++ks == C::kKStages) ks = 0, k_turn ^= 1;
     };
-    auto issue_pv = [&](bool first, bool tail) {
+    auto issue_pv = [&](bool first, bool tail, int steps) {
       if (kFp8) {
         w.wait(&ctl.wide_full[vs], v_turn);
       } else if (tail) {
@@ -239,9 +239,16 @@ kv_tree_keys_kernel(const __grid_constant__ CUtensorMap tm_k,
       const uint64_t dv = dv0 + static_cast<uint64_t>(vs * (32768 >> 4));
       const uint32_t acc0 = first ? 0u : 1u;
       if (elect_one()) {
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)   // both MN-major: 16 keys' rows per MMA
+        auto step = [&](int kk) {        // both MN-major: 16 keys' rows per MMA
           mma_bf16_ss(tm + C::kO, dv + 128 * kk, dp0 + C::kPitch * kk, id_pv, kk > 0 ? 1u : acc0);
+        };
+        if (steps >= 8) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) step(kk);
+        } else {
+#pragma unroll 1
+          for (int kk = 0; kk < steps; ++kk) step(kk);
+        }
         mma_commit(&ctl.pv_done[vs]);
       }
       __syncwarp();
@@ -255,12 +262,14 @@ kv_tree_keys_kernel(const __grid_constant__ CUtensorMap tm_k,
       const int n = __shfl_sync(0xffffffffu, seg.t1 - seg.t0, 0);
       // tiles from this one on hold nodes
       const int tail0 = __shfl_sync(0xffffffffu, (seg.seq - seg.n) / kTile - seg.t0, 0);
+      // groups of 16 keys from this tile on, so that the last stops at the sequence's end
+      const int groups = __shfl_sync(0xffffffffu, (seg.seq - seg.t0 * kTile + 15) / 16, 0);
       // S^T runs a tile ahead; the softmax has read the S^T two tiles back
       // when its P is waited for
       issue_s();
       for (int t = 0; t < n; ++t) {
         if (t + 1 < n) issue_s();
-        issue_pv(t == 0, t >= tail0);
+        issue_pv(t == 0, t >= tail0, groups - 8 * t);
       }
     }
     // drain: every MMA issued has completed before TMEM is freed
@@ -308,24 +317,26 @@ kv_tree_keys_kernel(const __grid_constant__ CUtensorMap tm_k,
           a.mask + static_cast<int64_t>(seg.q0 + max(my_node, 0)) * a.mask_words;
       float my_off = 0.0f;      // kPOffset - ref, 0 while unset
       // live columns that have met no visible key yet
-      uint32_t unset = __ballot_sync(0xffffffffu, my_node >= 0) & kAll;
+      const uint32_t live = __ballot_sync(0xffffffffu, my_node >= 0) & kAll;
+      uint32_t unset = live;
+      const int row0 = seg.rt * R + col0;
 
       for (int t = seg.t0; t < seg.t1; ++t, ++g) {
-        // ---- which columns see this thread's key: lane c collects column c's
-        // bits for the warp's 32 keys, then the warp transposes
+        // ---- which columns see this thread's key.  A chain: column c is row
+        // row0 + c, of node (row0 + c) / group, so columns from j group - row0
+        // on.  A tree: lane c collects column c's bits for the warp's 32 keys,
+        // then the warp transposes.
         const bool tail = t * kTile + kTile > ctx;      // the tile holds nodes
         uint32_t sees = kAll;
-        if (tail) {
+        if (tail && !a.mask) {
+          const int j = t * kTile + key - ctx;
+          if (j >= 0)
+            sees = j < seg.n ? live & ~low_bits(max(0, min(32, j * a.group - row0))) : 0u;
+        } else if (tail) {
           const int j0 = t * kTile + 32 * wq - ctx;     // node of the warp's first key
           uint32_t bits = j0 < 0 ? low_bits(-j0) : 0;
-          if (my_node >= 0 && j0 > -32 && j0 < seg.n) {
-            uint32_t m;
-            if (a.mask)
-              m = mask_bits(my_mask, a.mask_words, j0) & low_bits(seg.n - j0);
-            else
-              m = my_node < j0 ? 0u : low_bits(my_node - j0 + 1);
-            bits |= m;
-          }
+          if (my_node >= 0 && j0 > -32 && j0 < seg.n)
+            bits |= mask_bits(my_mask, a.mask_words, j0) & low_bits(seg.n - j0);
           sees = transpose_bits(bits, lane);
         }
 
@@ -509,12 +520,11 @@ kv_tree_keys_kernel(const __grid_constant__ CUtensorMap tm_k,
         group_sync(1 + C::kGroups, C::kSoftmaxThreads);   // P may be written again
       } else if (!w.aborted()) {
         const int64_t piece = (2 * static_cast<int64_t>(blockIdx.x) + (seg.t0 == 0)) * R + col0;
-        const int live = seg.n * a.group - seg.rt * R - col0;   // live columns of this group
         float* to = a.part_o + piece * kHeadDim + key;
 #pragma unroll
         for (int c = 0; c < kCols; ++c)
-          if (c < live) to[c * kHeadDim] = o[c];
-        if (wq == 0 && lane < kCols && lane < live)
+          if (live >> c & 1u) to[c * kHeadDim] = o[c];
+        if (wq == 0 && lane < kCols && (live >> lane & 1u))
           a.part_ml[piece + lane] =
               make_float2((unset >> lane & 1u) ? -INFINITY : kPOffset - my_off, l);
       }
@@ -679,7 +689,7 @@ kv_tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
       s_side ^= 1;
       if (++ks == C::kKStages) ks = 0, k_turn ^= 1;
     };
-    auto issue_pv = [&](bool first, bool tail) {
+    auto issue_pv = [&](bool first, bool tail, int steps) {
       if (kFp8) {
         w.wait(&ctl.wide_full[side], turn);
       } else if (tail) {
@@ -694,9 +704,16 @@ kv_tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
       const uint32_t p = tm + 128 * side, o = tm + C::kO + 128 * side;
       const uint32_t acc0 = first ? 0u : 1u;
       if (elect_one()) {
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)   // 16 keys: 8 columns of P, 16 rows of V
+        auto step = [&](int kk) {        // 16 keys: 8 columns of P, 16 rows of V
           mma_bf16_ts(o, p + 8 * kk, dv + 128 * kk, id_pv, kk > 0 ? 1u : acc0);
+        };
+        if (steps >= 8) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) step(kk);
+        } else {
+#pragma unroll 1
+          for (int kk = 0; kk < steps; ++kk) step(kk);
+        }
         mma_commit(&ctl.pv_done[side]);
       }
       __syncwarp();
@@ -709,11 +726,13 @@ kv_tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
       if (!__shfl_sync(0xffffffffu, static_cast<int>(go), 0)) break;
       const int n = __shfl_sync(0xffffffffu, seg.t1 - seg.t0, 0);
       const int tail0 = __shfl_sync(0xffffffffu, (seg.seq - seg.n) / kTile - seg.t0, 0);
+      // groups of 16 keys from this tile on, so that the last stops at the sequence's end
+      const int groups = __shfl_sync(0xffffffffu, (seg.seq - seg.t0 * kTile + 15) / 16, 0);
       // a group's next scores overwrite its P: they follow its product
       issue_s();
       if (n > 1) issue_s();
       for (int t = 0; t < n; ++t) {
-        issue_pv(t < 2, t >= tail0);
+        issue_pv(t < 2, t >= tail0, groups - 8 * t);
         if (t + 2 < n) issue_s();
       }
     }
@@ -942,7 +961,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_tree_join_kernel(const TreeAr
   for (int i0 = warp; i0 < kJoinRows; i0 += kJoinThreads / 32) {
     const int r = blockIdx.y * kJoinRows + i0;
     const int row = u.rt * R + r;
-    const int node = row / a.group;
+    const int node = node_of(a, row);
     if (u.pieces == 0 || node >= u.n) return;
     // piece i; the first CTA's piece is its last one, the others' their first
     auto at = [&](int i) { return (2 * static_cast<int64_t>(blockIdx.x + i) + (i == 0)) * R + r; };
@@ -1116,6 +1135,8 @@ cudaError_t launch_kv_tree(const KvTreeLaunch& p, cudaStream_t stream) {
   a.page_log2 = p.cache.page_log2;
   a.kv_heads = p.cache.heads;
   a.group = p.heads / p.cache.heads;
+  a.group_magic = a.group == 1 ? 0u
+                               : static_cast<uint32_t>(((uint64_t{1} << 32) + a.group - 1) / a.group);
   a.tables = p.tables;
   a.table_stride = p.table_stride;
   a.width = p.width;

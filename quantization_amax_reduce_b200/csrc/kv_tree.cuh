@@ -33,6 +33,7 @@ struct TreeArgs {
   const uint8_t* v;                      // V cache, for the non-finite rows
   int64_t page_stride, slot_stride, head_stride;   // elements
   int num_pages, page_log2, kv_heads, group;
+  uint32_t group_magic;                  // ceil(2^32 / group), 0 for a group of one
   const int32_t* tables;
   int64_t table_stride;
   int width;
@@ -160,6 +161,11 @@ __device__ __forceinline__ uint32_t low_bits(int n) {   // the n lowest bits, 0 
 // Work list: every role walks the same segments (a CTA's tiles of one unit).
 // ---------------------------------------------------------------------------
 
+// Node of a query row: row / group, exact while row * group < 2^32.
+__device__ __forceinline__ int node_of(const TreeArgs& a, int row) {
+  return a.group_magic ? static_cast<int>(__umulhi(static_cast<uint32_t>(row), a.group_magic)) : row;
+}
+
 struct Request {
   int seq, q0, n, tiles, row_tiles;
   __device__ __forceinline__ int work(int kv_heads) const { return kv_heads * row_tiles * tiles; }
@@ -263,6 +269,7 @@ template <int R, int kThreads>
 struct Walker {
   Finder<R, kThreads> find;
   int w, end;
+  int head = 0, rt = -1;     // the unit handed out last (its last tile was, too)
   __device__ __forceinline__ void init(const int* chunk, int ctas) {
     const int total = chunk[kThreads];
     const int per = tiles_per_cta(total, ctas);
@@ -270,20 +277,33 @@ struct Walker {
     w = static_cast<int>(min(from, static_cast<int64_t>(total)));
     end = static_cast<int>(min(from + per, static_cast<int64_t>(total)));
   }
+  // (the whole warp)
   __device__ __forceinline__ bool next(const TreeArgs& a, const int* chunk, Segment& s) {
     if (w >= end) return false;
+    const bool first = rt < 0;
+    const int old = find.b;
     find.seek(a, chunk, w);
     const Request& r = find.r;
+    s.t0 = 0;
+    if (first) {             // somewhere inside a unit
+      const int local = w - find.start;
+      const int unit = local / r.tiles;
+      head = unit / r.row_tiles;
+      rt = unit - head * r.row_tiles;
+      s.t0 = local - unit * r.tiles;
+    } else if (find.b != old) {
+      head = rt = 0;
+    } else if (++rt == r.row_tiles) {
+      rt = 0;
+      ++head;
+    }
     s.b = find.b;
     s.seq = r.seq;
     s.q0 = r.q0;
     s.n = r.n;
     s.tiles = r.tiles;
-    const int local = w - find.start;
-    const int unit = local / r.tiles;
-    s.head = unit / r.row_tiles;
-    s.rt = unit - s.head * r.row_tiles;
-    s.t0 = local - unit * r.tiles;
+    s.head = head;
+    s.rt = rt;
     s.t1 = min(s.tiles, s.t0 + (end - w));
     w += s.t1 - s.t0;
     return true;
@@ -392,7 +412,7 @@ struct QLoads {
 #pragma unroll
     for (int it = 0; it < kLoads; ++it) {
       const int row = s.rt * R + (first + it) * kRows + (tid >> 4);
-      const int node = row / a.group, gq = row - node * a.group;
+      const int node = node_of(a, row), gq = row - node * a.group;
       x[it] = make_uint4(0, 0, 0, 0);
       if (node < s.n)
         x[it] = __ldg(reinterpret_cast<const uint4*>(a.q + (s.q0 + node) * a.q_tok_stride +
@@ -507,7 +527,7 @@ __device__ __forceinline__ void store_q(const TreeArgs& a, const Segment& s, QLo
   }
   if (tid < R) {
     const int row = s.rt * R + tid;
-    const int node = row / a.group, gq = row - node * a.group;
+    const int node = node_of(a, row), gq = row - node * a.group;
     const bool live = node < s.n;
     rows.node[tid] = live ? node : -1;
     rows.out_row[tid] = live ? (s.q0 + node) * (a.kv_heads * a.group) + s.head * a.group + gq : -1;
@@ -517,37 +537,42 @@ __device__ __forceinline__ void store_q(const TreeArgs& a, const Segment& s, QLo
 }
 
 // ---------------------------------------------------------------------------
-// V of a tile.  In tiles that hold nodes, rows past the sequence become zeros,
-// and so do the non-finite elements of nodes, which a query that does not see
+// V of a tile.  In tiles that hold nodes, rows past the sequence, up to the 16
+// that a product takes at a time, become zeros, and so do the non-finite
+// elements of nodes, which a query that does not see
 // the node must not meet as 0 x Inf: the epilogue adds them.  Both return
 // whether this thread met such an element; pos0 = position of the tile's first
 // key, nodes begin at position ctx.
 // ---------------------------------------------------------------------------
 
 // E4M3 -> f16 into two 64-channel halves of 128-byte rows, 128-byte swizzle.
-// A thread's pieces of 16 channels: c = tid & 7 of rows 16 i + tid / 8.  They
-// become pieces 2 (c & 3) and + 1 of half c >> 2; the halves start with
-// different ones (no bank conflicts).  `taken` runs when the source is read,
-// `ready` before the destination is written.
+// A thread's pieces of 16 channels: for i = 0..7, piece 4 h + (lane & 3), h =
+// i & 1, of a row of the eight from 32 warp + 8 (i / 2) on.  It becomes pieces
+// 2 (lane & 3) and + 1 of half h.  Of the eight lanes that share a bank cycle
+// four have row p and four row p ^ 5: bit 2 apart their reads, bit 0 apart
+// their writes fall into different banks.  `taken` runs when the source is
+// read, `ready` before the destination is written.
 template <int kBatch, class Taken, class Ready>
 __device__ __forceinline__ bool widen_v(const uint8_t* src, uint8_t* wide, int tid, bool tail,
                                         int pos0, int ctx, int seq, Taken taken, Ready ready) {
   bool wild = false;
-  const int row = tid >> 3, c = tid & 7, odd = c >> 2;
-  uint8_t* to = wide + odd * 16384 + row * 128;
-  const int p0 = ((2 * (c & 3) + odd) ^ (row & 7)) << 4;
-  const int p1 = ((2 * (c & 3) + (odd ^ 1)) ^ (row & 7)) << 4;
+  const int c = tid & 3, p = (tid >> 3) & 3, r = (tid & 4) ? p ^ 5 : p;
+  const int row = (tid >> 5) * 32 + r;               // and 8 (i / 2) on
+  const uint8_t* from = src + row * 128;
+  const int f0 = (c ^ r) << 4, f1 = ((c + 4) ^ r) << 4;
+  uint8_t* to = wide + row * 128;
+  const int t0 = ((2 * c) ^ r) << 4, t1 = ((2 * c + 1) ^ r) << 4;
 #pragma unroll 1
   for (int i0 = 0; i0 < 8; i0 += kBatch) {
     uint4 x[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
-      x[i] = *reinterpret_cast<const uint4*>(src + ((i0 + i) * kPrepThreads + (tid ^ (row & 7))) * 16);
+      x[i] = *reinterpret_cast<const uint4*>(from + (i0 + i) / 2 * 1024 + (i & 1 ? f1 : f0));
     if (i0 + kBatch == 8) taken();
     if (tail) {
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        const int pos = pos0 + (i0 + i) * 16 + row;
+        const int pos = pos0 + row + (i0 + i) / 2 * 8;
         uint32_t* w = &x[i].x;
         uint32_t nan = 0;
 #pragma unroll
@@ -566,30 +591,28 @@ __device__ __forceinline__ bool widen_v(const uint8_t* src, uint8_t* wide, int t
     for (int i = 0; i < kBatch; ++i) {
       uint32_t f[8];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const uint32_t w = (&x[i].x)[u];
-        f[2 * u] = cvt_f16x2_from_e4m3x2(w & 0xFFFFu);
-        f[2 * u + 1] = cvt_f16x2_from_e4m3x2(w >> 16);
-      }
-      const uint4 lo = make_uint4(f[0], f[1], f[2], f[3]);
-      const uint4 hi = make_uint4(f[4], f[5], f[6], f[7]);
-      uint8_t* d = to + (i0 + i) * 2048;
-      *reinterpret_cast<uint4*>(d + p0) = odd ? hi : lo;
-      *reinterpret_cast<uint4*>(d + p1) = odd ? lo : hi;
+      for (int u = 0; u < 4; ++u) cvt_f16x4_from_e4m3x4((&x[i].x)[u], f[2 * u], f[2 * u + 1]);
+      uint8_t* d = to + (i & 1) * 16384 + (i0 + i) / 2 * 1024;
+      *reinterpret_cast<uint4*>(d + t0) = make_uint4(f[0], f[1], f[2], f[3]);
+      *reinterpret_cast<uint4*>(d + t1) = make_uint4(f[4], f[5], f[6], f[7]);
     }
   }
   fence_proxy_async();
   return wild;
 }
 
-// A bf16 tile that holds nodes, in place.
+// A bf16 tile that holds nodes, in place: 16 lanes a row.
 __device__ __forceinline__ bool mend_v(uint8_t* src, int tid, int pos0, int ctx, int seq) {
   bool wild = false;
-  for (int i = tid; i < 32768 / 16; i += kPrepThreads) {
-    const int pos = pos0 + ((i >> 3) & 127);
-    if (pos < ctx) continue;
-    uint4* p = reinterpret_cast<uint4*>(src + i * 16);
-    uint4 x = pos < seq ? *p : make_uint4(0, 0, 0, 0);
+  const int last = min(kTile, (seq - pos0 + 15) & ~15);
+  uint8_t* piece = src + ((tid >> 3) & 1) * 16384 + (tid & 7) * 16;
+  for (int row = max(0, ctx - pos0) + (tid >> 4); row < last; row += kPrepThreads / 16) {
+    uint4* p = reinterpret_cast<uint4*>(piece + row * 128);
+    if (pos0 + row >= seq) {
+      *p = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    uint4 x = *p;
     uint32_t* w = &x.x;
     uint32_t found = 0;
 #pragma unroll
@@ -598,7 +621,7 @@ __device__ __forceinline__ bool mend_v(uint8_t* src, int tid, int pos0, int ctx,
       w[u] &= ~m;
       found |= m;
     }
-    if (found || pos >= seq) *p = x;
+    if (found) *p = x;
     wild |= found != 0;
   }
   fence_proxy_async();

@@ -412,6 +412,13 @@ __device__ __forceinline__ uint32_t cvt_f16x2_from_e4m3x2(uint32_t x) {
   return d;
 }
 
+// Four E4M3 codes -> their exact f16 values, in order.
+__device__ __forceinline__ void cvt_f16x4_from_e4m3x4(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi) : "r"(x));
+}
+
 __device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
