@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 from typing import Dict, Iterable, List, Optional, Sequence, Tuple
@@ -581,40 +582,51 @@ def _launch_on(stream, device):
     return stream.cuda_stream, torch.cuda.stream(stream)
 
 
-def _int32(t, name: str, device, numel: Optional[int] = None) -> int:
+# (These calls take microseconds on the device, so their checks are lean: types
+# are compared by identity, sizes and strides read once.)
+_I32, _I64, _U8, _BF16, _F32 = (torch.int32, torch.int64, torch.uint8, torch.bfloat16,
+                                torch.float32)
+
+
+def _int32(t, name: str, device, numel: int = -1) -> int:
     """Pointer of a contiguous int32 tensor on ``device`` (of ``numel`` elements)."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device:
+    if not isinstance(t, torch.Tensor) or t.dtype is not _I32 or t.device != device:
         raise ValueError(f"{name} must be an int32 tensor on {device}")
-    if not t.is_contiguous() or (numel is not None and t.numel() != numel):
+    if not t.is_contiguous() or (numel >= 0 and t.numel() != numel):
         raise ValueError(f"{name} must be contiguous" +
-                         (f" and hold {numel} elements" if numel is not None else ""))
+                         (f" and hold {numel} elements" if numel >= 0 else ""))
     return t.data_ptr()
 
 
-def _block_tables(t, rows: int, device):
-    """(pointer, row stride, width) of int32 block tables [rows, width]."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device:
-        raise ValueError(f"block_tables must be an int32 tensor on {device}")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] < 1 or \
-            (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"block_tables must be [{rows}, width >= 1] with contiguous rows")
-    return t.data_ptr(), t.stride(0), t.shape[1]
+def _table(t, name: str, rows: int, device, least: int = 0):
+    """(pointer, row stride, width) of an int32 table [rows, width >= least]
+    with contiguous rows."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not _I32 or t.device != device:
+        raise ValueError(f"{name} must be an int32 tensor on {device}")
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or shape[1] < least:
+        raise ValueError(f"{name} must be [{rows}, width >= {least}]")
+    stride, inner = t.stride()
+    if inner != 1 and shape[1] > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), stride, shape[1]
 
 
 def _paged_cache(k_cache, v_cache):
-    """(pages, page_size, heads, strides, device) of a paged cache: uint8 (E4M3
-    codes) or bf16 [pages, page_size, heads, 128] views of any strides with
-    the channel contiguous."""
+    """(pages, page_size, heads, strides, E4M3?, device) of a paged cache: uint8
+    (E4M3 codes) or bf16 [pages, page_size, heads, 128] views of any strides
+    with the channel contiguous."""
     _require_cuda(k_cache, "k_cache")
     _require_cuda(v_cache, "v_cache")
-    shape, strides = k_cache.shape, k_cache.stride()
-    if k_cache.dtype not in (torch.uint8, torch.bfloat16) or v_cache.dtype != k_cache.dtype:
+    shape, strides, dtype, device = (k_cache.shape, k_cache.stride(), k_cache.dtype,
+                                     k_cache.device)
+    if (dtype is not _U8 and dtype is not _BF16) or v_cache.dtype is not dtype:
         raise ValueError("k_cache and v_cache must both be uint8 (E4M3 codes) or bfloat16")
-    if v_cache.shape != shape or v_cache.stride() != strides or v_cache.device != k_cache.device:
+    if v_cache.shape != shape or v_cache.stride() != strides or v_cache.device != device:
         raise ValueError("k_cache and v_cache must share shape, strides and device")
     if len(shape) != 4 or shape[3] != HEAD_DIM or strides[3] != 1:
         raise ValueError("a cache is [pages, page_size, heads, 128] with contiguous channels")
-    return shape[0], shape[1], shape[2], strides, k_cache.device
+    return shape[0], shape[1], shape[2], strides, dtype is _U8, device
 
 
 def _scale3(scale, name: str, fp8: bool, device) -> int:
@@ -626,7 +638,7 @@ def _scale3(scale, name: str, fp8: bool, device) -> int:
     if scale is None:
         return 0
     if isinstance(scale, torch.Tensor):
-        if scale.dtype != torch.float32 or scale.numel() != 3 or not scale.is_contiguous() or \
+        if scale.dtype is not _F32 or scale.numel() != 3 or not scale.is_contiguous() or \
                 scale.device != device:
             raise ValueError(f"{name} must be 3 contiguous fp32 values on {device}")
         return scale.data_ptr()
@@ -635,6 +647,13 @@ def _scale3(scale, name: str, fp8: bool, device) -> int:
 
 def _error_ptr(error, device) -> int:
     return 0 if error is None else _int32(error, "error", device, 1)
+
+
+@functools.lru_cache(maxsize=4096)
+def _tree_workspace(rows: int, max_q_len: int, max_seqlen: int, heads: int, kv_heads: int) -> int:
+    """int32 words of workspace (a function of the sizes alone)."""
+    return (lib().fp8attn_kv_tree_workspace_bytes(rows, max_q_len, max_seqlen, heads, kv_heads)
+            + 3) // 4
 
 
 def kv_assign_pages(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_tables: torch.Tensor,
@@ -654,32 +673,32 @@ def kv_assign_pages(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_tables
     free pages or inconsistent lengths change nothing and set ``error`` (see
     fp8attn_kv_assign_pages in fp8attn.h)."""
     _require_cuda(seq_lens, "seq_lens")
-    dev, rows = seq_lens.device, seq_lens.numel()
-    max_tokens = int(max_tokens)
+    dev, rows, max_tokens = seq_lens.device, seq_lens.numel(), int(max_tokens)
     if max_tokens < 0:
         raise ValueError("max_tokens must not be negative")
-    tables, table_stride, width = _block_tables(block_tables, rows, dev)
-    args = (_int32(seq_lens, "seq_lens", dev), _int32(new_lens, "new_lens", dev, rows), rows,
-            int(page_size), tables, table_stride, width, _int32(owned, "owned", dev, rows),
-            _int32(free_pages, "free_pages", dev), free_pages.numel(),
-            _int32(pool, "pool", dev, 2), max_tokens)
-    err = _error_ptr(error, dev)
+    tables, table_stride, width = _table(block_tables, "block_tables", rows, dev, 1)
+    seq, new = _int32(seq_lens, "seq_lens", dev), _int32(new_lens, "new_lens", dev, rows)
+    own, free = _int32(owned, "owned", dev, rows), _int32(free_pages, "free_pages", dev)
+    count, err = _int32(pool, "pool", dev, 2), _error_ptr(error, dev)
     handle, on = _launch_on(stream, dev)
     with on:
         if out is None:
             cu = seq_lens.new_empty(rows + 1)
-            slots = seq_lens.new_empty(max_tokens, dtype=torch.int64)
+            slots = seq_lens.new_empty(max_tokens, dtype=_I64)
             positions = seq_lens.new_empty(max_tokens)
         else:
             cu, slots, positions = out
-            _check_out(cu, "cu_new", torch.int32, rows + 1, dev)
-            _check_out(slots, "slots", torch.int64, max_tokens, dev)
-            _check_out(positions, "positions", torch.int32, max_tokens, dev)
+            _check_out(cu, "cu_new", _I32, rows + 1, dev)
+            _check_out(slots, "slots", _I64, max_tokens, dev)
+            _check_out(positions, "positions", _I32, max_tokens, dev)
         if rows == 0:
             cu.zero_()
-        _check(lib().fp8attn_kv_assign_pages(*args, cu.data_ptr(), slots.data_ptr(),
-                                             positions.data_ptr(), err, handle),
-               "fp8attn_kv_assign_pages")
+        status = lib().fp8attn_kv_assign_pages(
+            seq, new, rows, int(page_size), tables, table_stride, width, own, free,
+            free_pages.numel(), count, max_tokens, cu.data_ptr(), slots.data_ptr(),
+            positions.data_ptr(), err, handle)
+    if status:
+        raise FP8AttnError(status, "fp8attn_kv_assign_pages")
     return cu, slots, positions
 
 
@@ -692,30 +711,32 @@ def kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: tor
     fl32(x * scale), with ``quant_scale`` a device pointer (e.g.
     ``Context.static_quant_scale_ptr(layer)``) or a 3-element fp32 tensor
     {qs_q, qs_k, qs_v}; bf16 caches take no scale."""
-    pages, page_size, heads, strides, dev = _paged_cache(k_cache, v_cache)
+    pages, page_size, heads, strides, fp8, dev = _paged_cache(k_cache, v_cache)
     for name, t in (("k", k), ("v", v)):
         _require_cuda(t, name)
-        if t.dtype != torch.bfloat16 or t.device != dev:
+        if t.dtype is not _BF16 or t.device != dev:
             raise ValueError(f"{name} must be bfloat16 on {dev}")
-    if k.shape != v.shape or k.stride() != v.stride():
+    shape, steps = k.shape, k.stride()
+    if v.shape != shape or v.stride() != steps:
         raise ValueError("k and v must share shape and strides")
-    if k.dim() != 3 or k.shape[1] != heads or k.shape[2] != HEAD_DIM or k.stride(2) != 1:
+    if len(shape) != 3 or shape[1] != heads or shape[2] != HEAD_DIM or steps[2] != 1:
         raise ValueError(f"k and v must be [T, {heads}, 128] with contiguous channels")
-    T = k.shape[0]
-    if not isinstance(slots, torch.Tensor) or slots.dtype != torch.int64 or \
+    T = shape[0]
+    if not isinstance(slots, torch.Tensor) or slots.dtype is not _I64 or \
             slots.device != dev or slots.shape != (T,) or not slots.is_contiguous():
         raise ValueError(f"slots must be a contiguous int64 [{T}] tensor on {dev}")
-    scale = _scale3(quant_scale, "quant_scale", k_cache.dtype == torch.uint8, dev)
+    scale, err = _scale3(quant_scale, "quant_scale", fp8, dev), _error_ptr(error, dev)
     # the stride of a dimension of size one says nothing
-    tok_stride = k.stride(0) if T > 1 else heads * HEAD_DIM
-    head_stride = k.stride(1) if heads > 1 else HEAD_DIM
-    err = _error_ptr(error, dev)
+    tok_stride = steps[0] if T > 1 else heads * HEAD_DIM
+    head_stride = steps[1] if heads > 1 else HEAD_DIM
     handle, on = _launch_on(stream, dev)
     with on:
-        _check(lib().fp8attn_kv_write(
+        status = lib().fp8attn_kv_write(
             k.data_ptr(), v.data_ptr(), tok_stride, head_stride, slots.data_ptr(), T, heads,
             HEAD_DIM, k_cache.data_ptr(), v_cache.data_ptr(), strides[0], strides[1], strides[2],
-            pages, page_size, scale, err, handle), "fp8attn_kv_write")
+            pages, page_size, scale, err, handle)
+    if status:
+        raise FP8AttnError(status, "fp8attn_kv_write")
 
 
 def kv_tree_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -736,46 +757,47 @@ def kv_tree_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     a 3-element fp32 tensor {ds_q, ds_k, ds_v} for a uint8 (E4M3) cache; a
     bf16 cache takes none.  Returns bf16 [T, heads, 128] (a query that sees
     nothing: 0; rows of no request in a given ``out`` stay as they are)."""
-    pages, page_size, kv_heads, strides, dev = _paged_cache(k_cache, v_cache)
+    pages, page_size, kv_heads, strides, fp8, dev = _paged_cache(k_cache, v_cache)
     _require_cuda(q, "q")
-    if q.dtype != torch.bfloat16 or q.device != dev:
+    if q.dtype is not _BF16 or q.device != dev:
         raise ValueError(f"q must be bfloat16 on {dev}")
-    if q.dim() != 3 or q.shape[2] != HEAD_DIM or q.stride(2) != 1:
+    shape, steps = q.shape, q.stride()
+    if len(shape) != 3 or shape[2] != HEAD_DIM or steps[2] != 1:
         raise ValueError("q must be [T, heads, 128] with contiguous channels")
-    T, heads = q.shape[0], q.shape[1]
+    T, heads, _ = shape
     if heads < 1 or kv_heads < 1 or heads % kv_heads:
         raise ValueError(f"{heads} query heads are no multiple of {kv_heads} KV heads")
     _require_cuda(seq_lens, "seq_lens")
     rows = seq_lens.numel()
-    tables, table_stride, width = _block_tables(block_tables, rows, dev)
+    tables, table_stride, width = _table(block_tables, "block_tables", rows, dev, 1)
     seq, cu = _int32(seq_lens, "seq_lens", dev), _int32(cu_q, "cu_q", dev, rows + 1)
-    mask, words = 0, 0
+    mask = words = 0
     if tree_mask is not None:
-        if not isinstance(tree_mask, torch.Tensor) or tree_mask.dtype != torch.int64 or \
+        if not isinstance(tree_mask, torch.Tensor) or tree_mask.dtype is not _I64 or \
                 tree_mask.device != dev or tree_mask.dim() != 2 or tree_mask.shape[0] != T or \
                 tree_mask.shape[1] < 1 or not tree_mask.is_contiguous():
             raise ValueError(f"tree_mask must be a contiguous int64 [{T}, words] tensor on {dev}")
         mask, words = tree_mask.data_ptr(), tree_mask.shape[1]
-    scale = _scale3(descale, "descale", k_cache.dtype == torch.uint8, dev)
-    tok_stride = q.stride(0) if T > 1 else heads * HEAD_DIM
-    head_stride = q.stride(1) if heads > 1 else HEAD_DIM
+    scale, err = _scale3(descale, "descale", fp8, dev), _error_ptr(error, dev)
+    tok_stride = steps[0] if T > 1 else heads * HEAD_DIM
+    head_stride = steps[1] if heads > 1 else HEAD_DIM
     max_q_len, max_seqlen = int(max_q_len), int(max_seqlen)
-    err = _error_ptr(error, dev)
-    L = lib()
-    need = L.fp8attn_kv_tree_workspace_bytes(rows, max_q_len, max_seqlen, heads, kv_heads)
+    need = _tree_workspace(rows, max_q_len, max_seqlen, heads, kv_heads)
     handle, on = _launch_on(stream, dev)
     with on:
         if out is None:
-            out = q.new_empty(q.shape)
+            out = q.new_empty(shape)
         else:
-            _check_out(out, "out", torch.bfloat16, T * heads * HEAD_DIM, dev)
-        work = seq_lens.new_empty(need + 3 >> 2) if need else None
-        _check(L.fp8attn_kv_tree_fwd(
+            _check_out(out, "out", _BF16, T * heads * HEAD_DIM, dev)
+        work = seq_lens.new_empty(need) if need else None
+        status = lib().fp8attn_kv_tree_fwd(
             q.data_ptr(), tok_stride, head_stride, k_cache.data_ptr(), v_cache.data_ptr(),
             strides[0], strides[1], strides[2], pages, page_size, tables, table_stride, width,
             seq, cu, rows, max_q_len, max_seqlen, T, heads, kv_heads, HEAD_DIM, scale, mask,
-            words, float(softmax_scale), out.data_ptr(),
-            0 if work is None else work.data_ptr(), need, err, handle), "fp8attn_kv_tree_fwd")
+            words, softmax_scale, out.data_ptr(), work.data_ptr() if need else 0, 4 * need, err,
+            handle)
+    if status:
+        raise FP8AttnError(status, "fp8attn_kv_tree_fwd")
     return out
 
 
@@ -788,23 +810,21 @@ def kv_keep_path(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: tor
     its n_b = ``cu_q[b + 1] - cu_q[b]`` nodes, the last n_b of ``seq_lens[b]``
     positions, move to nodes 0, 1, ... of the cache, in place.  The request
     then holds seq_lens[b] - n_b + keep_lens[b] tokens."""
-    pages, page_size, heads, strides, dev = _paged_cache(k_cache, v_cache)
+    pages, page_size, heads, strides, _, dev = _paged_cache(k_cache, v_cache)
     _require_cuda(seq_lens, "seq_lens")
     rows = seq_lens.numel()
-    tables, table_stride, width = _block_tables(block_tables, rows, dev)
-    if not isinstance(paths, torch.Tensor) or paths.dtype != torch.int32 or \
-            paths.device != dev or paths.dim() != 2 or paths.shape[0] != rows or \
-            (paths.shape[1] > 1 and paths.stride(1) != 1):
-        raise ValueError(f"paths must be an int32 [{rows}, depth] tensor on {dev}")
-    args = (_int32(seq_lens, "seq_lens", dev), _int32(cu_q, "cu_q", dev, rows + 1), rows,
-            paths.data_ptr(), paths.stride(0), paths.shape[1],
-            _int32(keep_lens, "keep_lens", dev, rows), _error_ptr(error, dev))
+    tables, table_stride, width = _table(block_tables, "block_tables", rows, dev, 1)
+    path, path_stride, depth = _table(paths, "paths", rows, dev)
+    seq, cu = _int32(seq_lens, "seq_lens", dev), _int32(cu_q, "cu_q", dev, rows + 1)
+    keep, err = _int32(keep_lens, "keep_lens", dev, rows), _error_ptr(error, dev)
     handle, on = _launch_on(stream, dev)
     with on:
-        _check(lib().fp8attn_kv_keep_path(
+        status = lib().fp8attn_kv_keep_path(
             k_cache.data_ptr(), v_cache.data_ptr(), strides[0], strides[1], strides[2], pages,
-            page_size, k_cache.element_size(), heads, HEAD_DIM, tables, table_stride, width,
-            *args, handle), "fp8attn_kv_keep_path")
+            page_size, k_cache.element_size(), heads, HEAD_DIM, tables, table_stride, width, seq,
+            cu, rows, path, path_stride, depth, keep, err, handle)
+    if status:
+        raise FP8AttnError(status, "fp8attn_kv_keep_path")
 
 
 # ---------------------------------------------------------------------------
