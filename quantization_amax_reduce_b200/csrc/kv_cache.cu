@@ -40,7 +40,8 @@ __device__ __forceinline__ void raise_error(int32_t* err, uint32_t bits) {
 // ---------------------------------------------------------------------------
 
 constexpr int kPagesThreads = 512;
-constexpr int kTokensPerThread = 4;
+constexpr int kTokensPerThread = 4;   // neighbours share the search for their row
+constexpr int kPagesPerThread = 4;
 
 struct PagesArgs {
   const int32_t* seq;
@@ -160,13 +161,14 @@ __global__ void __launch_bounds__(kPagesThreads) assign_pages_kernel(const Pages
   auto want_of = [&](int b) {
     return static_cast<int>((static_cast<int64_t>(a.seq[b]) + page_mask) >> a.page_log2);
   };
-  auto dropped_page = [&](int k) {
-    const int b = row_of(s_drop, a.rows, k);
+  // the dropped page of rank k, of row b
+  auto dropped_of = [&](int k, int b) {
     return a.tables[b * a.table_stride + want_of(b) + (k - s_drop[b])];
   };
   // the page of wanted rank k; -1 (and the error bit) if the list holds no page there
   auto wanted_page = [&](int k) {
-    const int page = k < dropped ? dropped_page(k) : a.free_pages[count - 1 - (k - dropped)];
+    const int page = k < dropped ? dropped_of(k, row_of(s_drop, a.rows, k))
+                                 : a.free_pages[count - 1 - (k - dropped)];
     if (page >= 0 && page < a.num_pages) return page;
     raise_error(a.err, kErrPages);
     return -1;
@@ -174,12 +176,34 @@ __global__ void __launch_bounds__(kPagesThreads) assign_pages_kernel(const Pages
 
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b <= a.rows; b += kPagesThreads) a.cu[b] = refused ? 0 : s_cu[b];
-  for (int k = tid; k < wanted; k += step) {
-    const int b = row_of(s_grow, a.rows, k);
-    a.tables[b * a.table_stride + a.owned[b] + (k - s_grow[b])] = wanted_page(k);
+  for (int64_t k0 = static_cast<int64_t>(tid) * kPagesPerThread; k0 < wanted;
+       k0 += static_cast<int64_t>(step) * kPagesPerThread) {
+    int b = row_of(s_grow, a.rows, static_cast<int>(k0));
+#pragma unroll
+    for (int i = 0; i < kPagesPerThread; ++i) {
+      const int k = static_cast<int>(k0) + i;
+      if (k0 + i >= wanted) break;
+      while (s_grow[b + 1] <= k) ++b;
+      a.tables[b * a.table_stride + a.owned[b] + (k - s_grow[b])] = wanted_page(k);
+    }
   }
-  for (int k = wanted + tid; k < dropped; k += step)
-    a.free_pages[count + dropped - 1 - k] = dropped_page(k);
+  for (int64_t k0 = wanted + static_cast<int64_t>(tid) * kPagesPerThread; k0 < dropped;
+       k0 += static_cast<int64_t>(step) * kPagesPerThread) {
+    int b = row_of(s_drop, a.rows, static_cast<int>(k0));
+    int row[kPagesPerThread], page[kPagesPerThread];
+#pragma unroll
+    for (int i = 0; i < kPagesPerThread; ++i) {
+      const int k = static_cast<int>(min(k0 + i, static_cast<int64_t>(dropped) - 1));
+      while (s_drop[b + 1] <= k) ++b;
+      row[i] = b;
+    }
+#pragma unroll
+    for (int i = 0; i < kPagesPerThread; ++i)
+      page[i] = dropped_of(static_cast<int>(min(k0 + i, static_cast<int64_t>(dropped) - 1)), row[i]);
+#pragma unroll
+    for (int i = 0; i < kPagesPerThread; ++i)
+      if (k0 + i < dropped) a.free_pages[count + dropped - 1 - (k0 + i)] = page[i];
+  }
 
   // slots and positions, kTokensPerThread tokens at a time
   for (int64_t t0 = static_cast<int64_t>(tid) * kTokensPerThread; t0 < a.max_tokens;
@@ -230,14 +254,13 @@ __global__ void __launch_bounds__(kPagesThreads) assign_pages_kernel(const Pages
     }
   }
 
-  // commit: by the last CTA, when no other reads the old state any more
+  // commit: by the last CTA, when no other reads the old state any more (what
+  // the others read has arrived when they count, and nothing that they wrote is
+  // read here: no fence)
   if (gridDim.x > 1) {
     __syncthreads();
-    if (threadIdx.x == 0) {
-      __threadfence();
+    if (threadIdx.x == 0)
       s_last = atomicAdd(reinterpret_cast<unsigned int*>(a.pool + 1), 1u) == gridDim.x - 1;
-      __threadfence();
-    }
     __syncthreads();
     if (!s_last) return;
     if (threadIdx.x == 0) a.pool[1] = 0;
@@ -438,11 +461,16 @@ cudaError_t launch_assign_pages(const AssignPagesLaunch& p, cudaStream_t stream)
   a.slots = p.slots;
   a.positions = p.positions;
   a.err = p.err;
-  // enough CTAs for the tokens, and for the pages that rows may give back
-  const int64_t by_tokens = (static_cast<int64_t>(p.max_tokens) + kPagesThreads * kTokensPerThread - 1) /
-                            (kPagesThreads * kTokensPerThread);
-  const int64_t by_rows = (p.rows + kPagesThreads - 1) / kPagesThreads;
-  int64_t grid = by_tokens > by_rows ? by_tokens : by_rows;
+  // enough CTAs for the tokens, and for the pages that rows may take or give
+  // back (the pool's or the tables', whichever is fewer: two rounds of a CTA)
+  const int64_t by_tokens =
+      (static_cast<int64_t>(p.max_tokens) + kPagesThreads * kTokensPerThread - 1) /
+      (kPagesThreads * kTokensPerThread);
+  const int64_t held = static_cast<int64_t>(p.rows) * p.width;
+  const int64_t by_pages =
+      (held < p.num_pages ? held : p.num_pages) / (2 * kPagesThreads * kPagesPerThread);
+  int64_t grid = by_tokens > by_pages ? by_tokens : by_pages;
+  if (grid < 1) grid = 1;
   if (grid > 148) grid = 148;
   const size_t smem = 3 * (static_cast<size_t>(p.rows) + 1) * sizeof(int32_t);
   if (smem > 48 * 1024) {
