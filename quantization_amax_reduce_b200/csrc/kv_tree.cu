@@ -545,7 +545,10 @@ kv_tree_keys_kernel(const __grid_constant__ CUtensorMap tm_k,
 // holds a query row, so its maximum, sum, mask and rescaling are its own.  The
 // two softmax groups take alternate tiles of a unit, each with its own scores,
 // O, reference and sum, so that one's exponentials run beside the other's
-// products; they are joined like two pieces when the unit ends.  P lies in
+// products; they are joined like two pieces when the unit ends.  Up to 64 rows
+// lie on the lanes twice, and the second copies take the second half of each
+// tile's keys (their P is zero in the other half): half the exponentials a
+// thread, at the same products.  P lies in
 // TMEM over the first half of its scores, and feeds the product from there.
 // (The loops over 32 columns stay rolled: a CTA runs a unit's code once or
 // twice, and unrolled it waits for its instructions.)
@@ -560,7 +563,7 @@ struct RowsCfg {
   static constexpr int kPrepWarp = kMmaWarp + 1;
   static constexpr int kThreads = 32 * (kPrepWarp + kPrepWarps);
   static constexpr int kKV = kFp8 ? 16384 : 32768;
-  static constexpr int kKStages = kFp8 ? 4 : 3;
+  static constexpr int kKStages = 3;
   static constexpr int kVStages = kFp8 ? 3 : 2;
   static constexpr int kWide = kFp8 ? 2 : 0;
   // Q's remainders go into the same accumulator, unscaled, and each row has its
@@ -588,6 +591,7 @@ struct RowsControl {
   int chunk[C::kThreads + 1];
   UnitRows<128> rows[4];
   float2 ml[2][128];                     // {ref, sum} of each group's part of a row
+  float half[2][64][33];                 // 32 channels of the second copies' parts
 };
 
 template <bool kFp8>
@@ -742,7 +746,7 @@ kv_tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
     __syncwarp();
   } else if (warp >= C::kPrepWarp) {
     prepare<R, C::kThreads, kFp8, C::kLoScale, C::kVStages, 2>(
-        a, w, ctl.chunk, sq, sv, swide, ctl.rows, ctl.row_max, 2, ctl.q_full, ctl.v_full,
+        a, w, ctl.chunk, sq, sv, swide, ctl.rows, ctl.row_max, 4, ctl.q_full, ctl.v_full,
         ctl.v_empty, ctl.wide_full, ctl.flagged, threadIdx.x - 32 * C::kPrepWarp,
         [&](int g) { w.wait(&ctl.k_empty[g % C::kKStages], (g / C::kKStages) & 1); }, wait_pv);
   } else {
@@ -778,21 +782,33 @@ kv_tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
       bool set = false;         // whether the row has met a visible key
       uint64_t sum2[2] = {0, 0};
       const int g0 = g;
+      // the 32-key columns of a tile that this row takes
+      const bool doubled = is_doubled<R>(a, seg);
+      const int h0 = doubled ? wq & 2 : 0, h1 = doubled ? h0 + 2 : 4;
       for (int t = seg.t0; t < seg.t1; ++t, ++g) {
         if ((g & 1) != wg) continue;
         const bool tail = t * kTile + kTile > ctx;
+        // the row's view of the tile's four times 32 keys
+        uint32_t see0 = 0xffffffffu, see1 = see0, see2 = see0, see3 = see0;
+        if (tail) {
+          see0 = sees(t * kTile);
+          see1 = sees(t * kTile + 32);
+          see2 = sees(t * kTile + 64);
+          see3 = sees(t * kTile + 96);
+        }
+        auto seen = [&](int h) { return h == 0 ? see0 : h == 1 ? see1 : h == 2 ? see2 : see3; };
         w.wait(&ctl.s_full[wg], (g >> 1) & 1);
         tc_fence_after();
         // ---- the tile's maximum (the scores are read again below: 128 of
         // them and their exponentials do not fit the registers)
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-        for (int h = 0; h < 4; ++h) {
+        for (int h = h0; h < h1; ++h) {
           uint32_t u[32];
           tmem_ld32(t_s + 32 * h, u);
           tmem_ld_wait();
           if (tail) {
-            const uint32_t bits = sees(t * kTile + 32 * h);
+            const uint32_t bits = seen(h);
 #pragma unroll
             for (int c = 0; c < 32; ++c)
               if (!(bits >> c & 1u)) u[c] = 0xFF800000u;
@@ -828,11 +844,11 @@ kv_tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
         // ---- P: 32 scores become 16 words over scores that were read already
         const uint64_t f2 = f2_pack(factor, factor), o2 = f2_pack(off, off);
 #pragma unroll 1
-        for (int h = 0; h < 4; ++h) {
+        for (int h = h0; h < h1; ++h) {
           uint32_t u[32], p[16];
           tmem_ld32(t_s + 32 * h, u);
           tmem_ld_wait();
-          const uint32_t bits = tail ? sees(t * kTile + 32 * h) : 0xffffffffu;
+          const uint32_t bits = seen(h);
 #pragma unroll
           for (int c = 0; c < 32; c += 2) {
             float x0, x1;
@@ -847,12 +863,19 @@ kv_tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
           }
           tmem_st16(t_s + 16 * h, p);
         }
+        if (doubled) {   // the other half's keys
+          uint32_t zero[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) zero[c] = 0;
+          tmem_st32(t_s + 32 - 16 * h0, zero);
+        }
         tmem_st_wait();
         tc_fence_before();
         w.arrive(&ctl.p_full[wg]);
       }
 
-      // ---- epilogue: group wg takes channels 64 wg .. of both groups' parts
+      // ---- epilogue: group wg takes channels 64 wg .. of a row's parts: both
+      // groups', and with doubled rows the copy's
       {
         float s0, s1;
         f2_unpack(f2_add(sum2[0], sum2[1]), s0, s1);
@@ -865,16 +888,19 @@ kv_tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
       group_sync(1, C::kSoftmaxThreads);
       const bool has[2] = {n > 1 || (g0 & 1) == 0, n > 1 || (g0 & 1) == 1};
       float ref = -INFINITY, l = 0.0f, scale[2] = {0.0f, 0.0f};
+      const int other = doubled ? row ^ 64 : row;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        if (has[i]) ref = fmaxf(ref, ctl.ml[i][row].x);
+        if (has[i]) ref = fmaxf(ref, fmaxf(ctl.ml[i][row].x, ctl.ml[i][other].x));
+      // no visible key: ref = -inf, O = 0, l = 0 (NaN scores only: l = NaN)
+      auto weight = [&](float x) { return x == -INFINITY ? 1.0f : ex2_approx(x - ref); };
 #pragma unroll
       for (int i = 0; i < 2; ++i)
         if (has[i]) {
-          const float2 part = ctl.ml[i][row];
-          // no visible key: ref = -inf, O = 0, l = 0 (NaN scores only: l = NaN)
-          scale[i] = part.x == -INFINITY ? 1.0f : ex2_approx(part.x - ref);
-          l = fmaf(scale[i], part.y, l);
+          const float2 mine = ctl.ml[i][row], theirs = ctl.ml[i][other];
+          scale[i] = weight(mine.x);
+          l = fmaf(scale[i], mine.y, l);
+          if (doubled) l = fmaf(weight(theirs.x), theirs.y, l);
         }
       const bool flagged =
           *const_cast<volatile int*>(&ctl.flagged[(unit + 1) & 3]) == unit + 1;
@@ -882,22 +908,37 @@ kv_tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
       const float inv = l == 0.0f ? 0.0f : ds_v / l;
       const int out_row = rows.out_row[row];
       const int64_t piece = (2 * static_cast<int64_t>(blockIdx.x) + (seg.t0 == 0)) * R + row;
-      const bool live = out_row >= 0 && !w.aborted();
+      const bool copy = doubled && row >= 64;
+      const bool live = out_row >= 0 && !copy && !w.aborted();
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
         const int d0 = 64 * wg + 32 * h;
         float o[32];
 #pragma unroll
         for (int c = 0; c < 32; ++c) o[c] = 0.0f;
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < 2; ++i)
           if (has[i]) {
+            const float s = i ? scale[1] : scale[0];
             uint32_t u[32];
             tmem_ld32(tmem + lane_off + C::kO + 128 * i + d0, u);
             tmem_ld_wait();
 #pragma unroll
-            for (int c = 0; c < 32; ++c) o[c] = fmaf(scale[i], __uint_as_float(u[c]), o[c]);
+            for (int c = 0; c < 32; ++c) o[c] = fmaf(s, __uint_as_float(u[c]), o[c]);
           }
+        if (doubled) {
+          float* part = ctl.half[wg][row & 63];
+          if (copy) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) part[c] = o[c];
+          }
+          group_sync(2 + wg, 128);
+          if (!copy) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] += part[c];
+          }
+          group_sync(2 + wg, 128);
+        }
         if (flagged) {
           for (int pos = max(ctx, seg.t0 * kTile); pos < min(seg.seq, seg.t1 * kTile); ++pos) {
             const int id = a.tables[seg.b * a.table_stride + (pos >> a.page_log2)];

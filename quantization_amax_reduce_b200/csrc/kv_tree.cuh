@@ -397,6 +397,13 @@ __device__ __forceinline__ void produce(const TreeArgs& a, const Waits& w, const
 }
 
 // ---------------------------------------------------------------------------
+// 128-row tiles with at most 64 rows hold them twice: rows 64 to 127 are rows 0
+// to 63 again, and take the second half of a tile's keys.
+template <int R>
+__device__ __forceinline__ bool is_doubled(const TreeArgs& a, const Segment& s) {
+  return R == 128 && s.n * a.group - s.rt * R <= 64;
+}
+
 // Q of a unit: a half warp per row, 8 channels a lane, four rows of a half warp
 // at a time, the first four loaded a unit ahead.  K-major rows of 128 bytes,
 // 128-byte swizzle; bf16: two 64-channel halves; E4M3: hi tile, then the
@@ -409,9 +416,10 @@ struct QLoads {
   static constexpr int kAll = R / kRows, kLoads = kAll < 4 ? kAll : 4;
   uint4 x[kLoads];
   __device__ __forceinline__ void load(const TreeArgs& a, const Segment& s, int tid, int first) {
+    const int same = is_doubled<R>(a, s) ? 63 : R - 1;
 #pragma unroll
     for (int it = 0; it < kLoads; ++it) {
-      const int row = s.rt * R + (first + it) * kRows + (tid >> 4);
+      const int row = s.rt * R + (((first + it) * kRows + (tid >> 4)) & same);
       const int node = node_of(a, row), gq = row - node * a.group;
       x[it] = make_uint4(0, 0, 0, 0);
       if (node < s.n)
@@ -526,7 +534,7 @@ __device__ __forceinline__ void store_q(const TreeArgs& a, const Segment& s, QLo
     if (!kFp8 && tid == 0) rows.one_factor = 1;
   }
   if (tid < R) {
-    const int row = s.rt * R + tid;
+    const int row = s.rt * R + (is_doubled<R>(a, s) ? tid & 63 : tid);
     const int node = node_of(a, row), gq = row - node * a.group;
     const bool live = node < s.n;
     rows.node[tid] = live ? node : -1;
