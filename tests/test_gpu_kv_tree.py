@@ -103,7 +103,301 @@ def run(s, **kw):
     ([90], [20], 2, 2, 8),                   # the smallest pages; 32 columns
     ([1500, 40], [2, 30], 32, 8, 256),       # pages larger than a tile
     ([2100], [3], 4, 1, 1024),
+    ([300, 1], [9, 1], 4, 1, 16),            # 36 rows: two copies on the lanes
+    ([513], [16], 4, 1, 32),                 # 64 rows, one key in the fifth tile
+    ([400], [13], 5, 1, 16),                 # 65 rows
+    ([640, 129], [16, 17], 8, 1, 64),        # 128 rows; 136: a second tile of 8
+    ([5000], [3], 4, 2, 64),                 # cut over many CTAs
+    ([3000, 2900], [10, 1], 8, 2, 16),       # the same with 40 rows a KV head
+    ([2500], [20], 8, 1, 128),               # and with 160
 ])
 def test_against_64_bits(seq, nodes, hq, hkv, page, fp8):
     s = make(hash((tuple(seq), hq)) % 1000, seq, nodes, hq, hkv, page, fp8, head_major=page > 32)
     check(run(s), *expect(s))
+
+
+def brute_fill(s, what):
+    """Overwrites every slot that no request holds, and the rest of last pages."""
+    held = np.zeros(s["values"][0].shape[:2], dtype=bool)
+    page = held.shape[1]
+    for b, n in enumerate(s["seq"]):
+        for p in range(int(n)):
+            held[s["tables"][b][p // page], p % page] = True
+    at = torch.from_numpy(np.argwhere(~held)).to(DEV)
+    for c in s["caches"]:
+        c[at[:, 0], at[:, 1]] = what
+
+
+def set_kv(s, t, b, pos, channel, value):
+    """K (t = 0) or V (1) of request b's position, one channel of every head."""
+    page = s["values"][t].shape[1]
+    where = s["tables"][b][pos // page], pos % page
+    if s["fp8"]:
+        assert np.isnan(value)
+        s["caches"][t][where][:, channel] = NAN_CODE
+    else:
+        s["caches"][t][where][:, channel] = value
+    s["values"][t][where][:, channel] = value
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("nodes,hq,hkv", [(4, 4, 2), (20, 2, 2), (20, 4, 2), (33, 4, 1), (100, 2, 2)])
+def test_masks_with_empty_rows_and_several_words(nodes, hq, hkv, fp8):
+    s = make(nodes, [nodes, nodes + 200], [nodes, nodes], hq, hkv, 16, fp8)
+    s["mask"][2] = 0                       # sees nothing at all
+    s["mask"][nodes + 1] = 0               # sees the context alone
+    s["mask"][nodes - 1] = np.uint64(1)    # sees the root, not itself
+    if nodes > 64:
+        s["mask"][nodes - 2] = [0, 1 << 20]       # a node of the second word alone
+    # bits past the nodes mean nothing
+    s["mask"][0, -1] |= np.uint64(1) << np.uint64(63)
+    want, tol = expect(s)
+    assert (want[2] == 0).all()
+    got = run(s)
+    assert (got[2] == 0).all()
+    check(got, want, tol)
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("nodes,hq,hkv", [(4, 4, 2), (20, 2, 2), (20, 4, 2), (33, 4, 1)])
+def test_non_finite_values_in_hidden_places(nodes, hq, hkv, fp8):
+    """NaN and Inf in slots of no request, and in nodes that a query does not
+    see, do not touch it; a query that sees them shows them."""
+    s = make(nodes + 7, [nodes + 130, nodes + 61], [nodes, nodes], hq, hkv, 16, fp8)
+    brute_fill(s, NAN_CODE if fp8 else float("nan"))
+    first = 130
+    bad = float("nan") if fp8 else float("inf")
+    set_kv(s, 1, 0, first + 1, 5, bad)               # V of node 1 of request 0
+    set_kv(s, 1, 0, first + 2, 9, float("nan"))      # V of node 2
+    set_kv(s, 0, 0, first + 3, 17, float("nan"))     # K of node 3
+    sees = (s["mask"][:nodes, :1] >> np.arange(min(nodes, 64), dtype=np.uint64)) & 1
+    got = run(s).double().cpu().numpy()
+    want, tol = expect(s)
+    for i in range(nodes):
+        if sees[i, 3]:
+            assert np.isnan(got[i]).all()
+            want[i], got[i] = 0, 0
+            continue
+        for node, channel in ((1, 5), (2, 9)):
+            if sees[i, node]:
+                v = got[i, :, channel]
+                assert np.isnan(v).all() if node == 2 or fp8 else (v == np.inf).all()
+                want[i, :, channel] = got[i, :, channel] = 0
+    assert np.isfinite(want).all()
+    check(torch.from_numpy(got), want, np.nan_to_num(tol, nan=1.0, posinf=1.0))
+    # the other request never met any of it
+    check(torch.from_numpy(got[nodes:]), want[nodes:], tol[nodes:])
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("nodes,hq,hkv", [(1, 8, 1), (4, 5, 1), (12, 4, 1), (30, 4, 1)])
+def test_references_that_move_and_far_tails(nodes, hq, hkv, fp8):
+    """Scores that grow along the sequence move the reference again and again;
+    a sink key 2^-17 above thousands of equal ones must not swallow them."""
+    L = 1500
+    s = make(nodes, [L], [nodes], hq, hkv, 32, fp8, tree=False)
+    ramp = np.linspace(0.02, 1.0, L)
+    page = 32
+    q = s["q"].float()
+    q[:] = torch.sign(q) * 2.0
+    s["q"] = q.to(torch.bfloat16)
+    for p in range(L):
+        at = s["tables"][0][p // page], p % page
+        k = s["values"][0][at]
+        k[:] = np.sign(s["q"][0, 0].double().numpy()) * ramp[p] * (64 if fp8 else 1)
+    c = torch.from_numpy(s["values"][0])
+    c = c.to(torch.float8_e4m3fn) if fp8 else c.to(torch.bfloat16)
+    s["values"][0][:] = c.double().numpy()
+    s["caches"][0] = (c.view(torch.uint8) if fp8 else c).to(DEV)
+    check(run(s), *expect(s))
+    # the sink: one key along q, the others orthogonal to it (zero)
+    s["values"][0][:] = 0
+    at = s["tables"][0][3 // page], 3 % page
+    unit = np.sign(s["q"][0, 0].double().numpy())
+    scale = 11.78 * np.sqrt(128) / (256 * float(s["ds"][1]))     # exp(11.78) = 2^17
+    c = torch.from_numpy(unit * scale)
+    c = c.to(torch.float8_e4m3fn) if fp8 else c.to(torch.bfloat16)
+    s["values"][0][at] = c.double().numpy()
+    s["caches"][0].zero_()
+    s["caches"][0][at] = (c.view(torch.uint8) if fp8 else c).to(DEV)
+    check(run(s), *expect(s))
+
+
+@pytest.mark.parametrize("nodes,hq,hkv", [(6, 2, 1), (6, 4, 1), (12, 4, 1), (40, 4, 1)])
+def test_query_rows_of_very_different_sizes(nodes, hq, hkv):
+    """E4M3: rows that cannot share a scale, rows of zeros, one with an infinity."""
+    s = make(5, [200], [nodes], hq, hkv, 16, True, tree=False)
+    size = torch.tensor([2.0 ** ((i * 7) % 23 - 11) for i in range(nodes)])
+    s["q"] = (s["q"].float() * size[:, None, None]).to(torch.bfloat16)
+    s["q"][3] = 0
+    want, tol = expect(s)
+    check(run(s), want, tol)
+    s["q"][2, 0, 77] = float("inf")
+    got = run(s)
+    assert torch.isnan(got[2, 0]).all()
+    got[2, 0] = 0
+    want[2, 0] = 0
+    check(got, want, tol)
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+def test_many_requests_some_without_queries(fp8):
+    r = np.random.Generator(np.random.PCG64(1))
+    B = 1100
+    nodes = [int(x) for x in r.integers(0, 4, B)]
+    seq = [n + int(x) for n, x in zip(nodes, r.integers(0, 40, B))]
+    seq[17] = 700
+    s = make(3, seq, nodes, 2, 1, 16, fp8, tree=False)
+    check(run(s), *expect(s))
+
+
+def test_strided_queries_a_scale_and_rows_of_no_request():
+    s = make(9, [300, 20], [5, 3], 8, 2, 64, True)
+    args = to_dev(s)
+    T = s["q"].shape[0]
+    wide = torch.zeros(T + 4, 3, 8, 128, dtype=torch.bfloat16, device=DEV)
+    wide[:T, 1] = args[0]
+    wide[T:, 1] = 7
+    out = torch.full((T + 4, 8, 128), 5.0, dtype=torch.bfloat16, device=DEV)
+    mask = torch.cat([args[9], args[9][:4]])
+    got = qar.kv_tree_fwd(wide[:, 1], *args[1:9], mask, 0.03, out=out)
+    assert got is out and (out[T:] == 5).all()
+    check(out[:T], *expect(s, np.float64(np.float32(0.03))))
+
+
+def test_bad_requests_are_left_out_and_reported():
+    s = make(4, [40, 50, 60, 70], [4, 5, 6, 7], 4, 2, 16, True, tree=False)
+    want, tol = expect(s)
+    args = to_dev(s)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+
+    def attempt(**change):
+        a = list(args)
+        for i, v in change.items():
+            a[int(i[1:])] = v
+        out = torch.full(args[0].shape, 9.0, dtype=torch.bfloat16, device=DEV)
+        qar.kv_tree_fwd(*a, out=out, error=err)
+        torch.cuda.synchronize()
+        return out, qar.read_error_word(err)
+
+    seq = args[4].clone()
+    seq[1] = 4                                    # shorter than its five queries
+    seq[2] = 16 * args[3].shape[1] + 1            # beyond the block table
+    out, status = attempt(a4=seq, a7=4000)
+    assert status == 6 and (out[4:15] == 9).all()
+    check(out[:4], want[:4], tol[:4])
+    check(out[15:], want[15:], tol[15:])
+    out, status = attempt(a6=6)                   # the last request has seven
+    assert status == 6 and (out[15:] == 9).all()
+    check(out[:15], want[:15], tol[:15])
+    out, status = attempt(a7=60)                  # and is longer than 60
+    assert status == 6 and (out[15:] == 9).all()
+    cu = args[5].clone()
+    cu[4] = 23                                    # beyond the queries
+    out, status = attempt(a5=cu)
+    assert status == 6 and (out[15:] == 9).all()
+    # a page id outside the cache reads as zeros
+    tables = args[3].clone()
+    tables[3, 1], tables[0, 2] = 10 ** 6, -3
+    out, status = attempt(a3=tables)
+    assert status == 7
+    zero = len(s["values"][0])
+    s["values"] = [np.concatenate([v, np.zeros_like(v[:1])]) for v in s["values"]]
+    s["tables"][3, 1], s["tables"][0, 2] = zero, zero
+    check(out, *expect(s))
+
+
+def test_argument_checks_launch_nothing():
+    s = make(2, [40], [4], 4, 2, 16, True)
+    a = to_dev(s)
+    n0 = qar.launch_count()
+
+    def refuse(match, **change):
+        b = list(a)
+        kw = {}
+        for k, v in change.items():
+            if k[0] == "a" and k[1:].isdigit():
+                b[int(k[1:])] = v
+            else:
+                kw[k] = v
+        with pytest.raises((ValueError, qar.FP8AttnError), match=match):
+            qar.kv_tree_fwd(*b, **kw)
+
+    refuse("CUDA", a0=a[0].cpu())
+    refuse("bfloat16", a0=a[0].float())
+    refuse("heads", a0=a[0][:, :3])
+    refuse("128", a0=a[0][..., :64])
+    refuse("both be", a1=a[1].view(torch.int8), a2=a[2].view(torch.int8))
+    refuse("share", a2=a[2][:2])
+    refuse("block_tables", a3=a[3].long())
+    refuse("block_tables", a3=a[3][:, 0])
+    refuse("seq_lens", a4=a[4].long())
+    refuse("cu_q", a5=a[5][:1])
+    refuse("needed", a8=None)
+    refuse("tree_mask", a9=a[9][:2])
+    refuse("tree_mask", a9=a[9].int())
+    refuse("invalid", softmax_scale=-1.0)
+    refuse("invalid", softmax_scale=float("nan"))
+    refuse("needed", out=torch.zeros(3, 4, 128, dtype=torch.bfloat16, device=DEV))
+    refuse("int32", error=torch.zeros(1, device=DEV))
+    bf = [x.view(torch.bfloat16)[..., :64].contiguous() for x in a[1:3]]
+    refuse("128", a1=bf[0], a2=bf[1])
+    odd = torch.zeros(4, 24, 2, 128, dtype=torch.uint8, device=DEV)
+    refuse("unsupported", a1=odd, a2=odd)
+    assert qar.launch_count() == n0
+
+
+def test_same_bits_again_on_another_stream_and_replayed():
+    """Results do not depend on timing: calls repeated, overlapping on two
+    streams, captured and replayed with other lengths give the same bits."""
+    s = make(8, [6000, 400, 1, 77], [7, 1, 1, 4], 16, 2, 64, True, tree=False)
+    big = make(9, [3000, 900], [30, 20], 16, 2, 64, True)
+    args, more = to_dev(s), to_dev(big)
+    one, two = qar.kv_tree_fwd(*args), qar.kv_tree_fwd(*more)
+    assert torch.equal(one, qar.kv_tree_fwd(*args))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = []
+    for _ in range(10):
+        outs.append((qar.kv_tree_fwd(*args, stream=streams[0]),
+                     qar.kv_tree_fwd(*more, stream=streams[1])))
+    torch.cuda.synchronize()
+    for a, b in outs:
+        assert torch.equal(a, one) and torch.equal(b, two)
+    raw = qar.kv_tree_fwd(*args, stream=streams[0].cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(raw, one)
+    # two graphs over the same inputs and outputs, replayed with other lengths
+    args[7] = 6400
+    out = torch.empty_like(one)
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            qar.kv_tree_fwd(*args, out=out)
+        graphs.append(g)
+    for lens in ([6000, 400, 1, 77], [130, 390, 1, 4], [7, 1, 1, 64]):
+        args[4].copy_(torch.tensor(lens, dtype=torch.int32))
+        want = qar.kv_tree_fwd(*args)
+        for g in graphs:
+            out.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want)
+
+
+def test_empty_calls():
+    s = make(2, [40], [4], 4, 2, 16, False)
+    a = to_dev(s)
+    n0 = qar.launch_count()
+    none = torch.zeros(0, dtype=torch.int32, device=DEV)
+    out = qar.kv_tree_fwd(a[0][:0], a[1], a[2], a[3][:0], none, torch.zeros(1, dtype=torch.int32,
+                                                                         device=DEV), 0, 0)
+    assert out.shape == (0, 4, 128) and qar.launch_count() == n0
+    # requests without queries, and no keys at all
+    zero = torch.zeros(2, dtype=torch.int32, device=DEV)
+    out = torch.full((1, 4, 128), 3.0, dtype=torch.bfloat16, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    qar.kv_tree_fwd(a[0][:1], a[1], a[2], a[3], zero[:1], zero, 0, 0, out=out, error=err)
+    torch.cuda.synchronize()
+    assert (out == 3).all() and qar.read_error_word(err) == 0
