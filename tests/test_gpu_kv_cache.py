@@ -152,6 +152,38 @@ def test_assign_pages_captured_at_a_fixed_size():
     assert qar.read_error_word(d.err) == 0
 
 
+def test_assign_pages_of_two_threads_with_many_rows():
+    """Both calls need more shared memory than a launch gets unasked, in
+    different amounts: neither may take the other's away."""
+    import threading
+    failed = []
+
+    def work(rows):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                p = ref.Pool(rows, 2, 2 * rows, 16)
+                d = DevicePool(p)
+                seq = np.full(rows, 20)
+                new = np.zeros(rows, dtype=np.int64)
+                args = (dev32(seq), dev32(new), d.tables, d.owned, d.free, d.pool, 16, 0)
+                for _ in range(400):
+                    qar.kv_assign_pages(*args, error=d.err)
+                stream.synchronize()
+                assert qar.read_error_word(d.err) == 0
+                p.assign(seq, new, 0)
+                d.check(p)
+        except Exception as e:   # noqa: BLE001 (handed to the test)
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(rows,)) for rows in (16384, 4500)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+
+
 # ---------------------------------------------------------------------------
 # write
 # ---------------------------------------------------------------------------
