@@ -254,13 +254,16 @@ __global__ void __launch_bounds__(kPagesThreads) assign_pages_kernel(const Pages
     }
   }
 
-  // commit: by the last CTA, when no other reads the old state any more (what
-  // the others read has arrived when they count, and nothing that they wrote is
-  // read here: no fence)
+  // commit: by the last CTA, when no other reads the old state any more (the
+  // barriers and the counter's acquire and release order their reads before it)
   if (gridDim.x > 1) {
     __syncthreads();
-    if (threadIdx.x == 0)
-      s_last = atomicAdd(reinterpret_cast<unsigned int*>(a.pool + 1), 1u) == gridDim.x - 1;
+    if (threadIdx.x == 0) {
+      uint32_t before;
+      asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
+                   : "=r"(before) : "l"(a.pool + 1) : "memory");
+      s_last = before == gridDim.x - 1;
+    }
     __syncthreads();
     if (!s_last) return;
     if (threadIdx.x == 0) a.pool[1] = 0;
