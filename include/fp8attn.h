@@ -628,7 +628,8 @@ fp8attn_status fp8attn_kv_tree_fwd(const void* q, int64_t q_tok_stride, int64_t 
  * not rise or leaves [0, n_b), bad lengths: the request is left out), PAGES
  * (a page id outside the cache: that node does not move).
  * Errors: INVALID, UNSUPPORTED (head_dim != 128, page_size, strides or
- * alignment), CUDA.  rows == 0 or depth == 0 launches nothing. */
+ * alignment, num_kv_heads >= 2^17), CUDA.  rows == 0 or depth == 0 launches
+ * nothing. */
 fp8attn_status fp8attn_kv_keep_path(void* k_cache, void* v_cache, int64_t page_stride,
                                     int64_t slot_stride, int64_t cache_head_stride, int num_pages,
                                     int page_size, int elem_bytes, int num_kv_heads, int head_dim,

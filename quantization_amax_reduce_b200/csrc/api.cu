@@ -856,7 +856,7 @@ fp8attn_status fp8attn_kv_keep_path(void* k_cache, void* v_cache, int64_t page_s
       check_cache(k_cache, v_cache, page_stride, slot_stride, cache_head_stride, num_pages,
                   page_size, num_kv_heads, head_dim, elem_bytes == 1, &p.cache);
   if (st != FP8ATTN_OK || rows == 0 || depth == 0) return st;
-  if (num_kv_heads > 1 << 18) return FP8ATTN_ERR_UNSUPPORTED;
+  if (num_kv_heads >= 1 << 17) return FP8ATTN_ERR_UNSUPPORTED;   // blocks in y
   if (rows > 1 && (table_stride < table_width || path_stride < depth)) return FP8ATTN_ERR_INVALID;
   if (!d_block_tables || !d_seq_lens || !d_cu_q || !d_paths || !d_keep_lens)
     return FP8ATTN_ERR_INVALID;

@@ -119,6 +119,13 @@ def test_keep_path_refusals(L):
     assert call(f, base, depth=0) == OK
 
 
+def test_keep_path_heads_beyond_the_grid(L):
+    heads = 1 << 18   # 32 bf16 vectors a head, 128 a block: 65536 blocks, one too many
+    args = (P(16), P(16), 8 * 128 * heads, 128 * heads, 128, 32, 8, 2, heads, 128, P(16), 8, 8,
+            P(16), P(16), 3, P(16), 5, 5, P(16), None, None)
+    assert L.fp8attn_kv_keep_path(*args) == UNSUPPORTED
+
+
 def test_static_pointers_need_a_context(L):
     assert L.fp8attn_static_quant_scale_ptr(None, 0) is None
     assert L.fp8attn_static_descale_ptr(None, 0) is None
