@@ -585,7 +585,10 @@ size_t fp8attn_kv_tree_workspace_bytes(int rows, int max_q_len, int max_seqlen, 
  * of them if bit m % 64 of d_tree_mask[i][m / 64] is set (int64 [total_q,
  * mask_words], rows cu_q[b] + i); without a mask, m <= i.  Query head h reads
  * KV head h / (num_heads / num_kv_heads).  A query that sees nothing gives 0;
- * K and V that a query does not see do not touch it, Inf and NaN included.
+ * K and V that a query does not see do not touch it, Inf and NaN included (a
+ * non-finite value that it does see makes its output non-finite: Inf may come
+ * out as NaN).  Requests may share pages, but not table rows (table_stride >=
+ * table_width).
  *   out[i] = ds_v sum_j p_j v_j / sum_j p_j,
  *   p_j = exp(softmax_scale ds_k q_i . k_j - max)
  * d_descale_qkv: device {ds_q, ds_k, ds_v} for an E4M3 cache (q is bf16, ds_q
@@ -603,7 +606,9 @@ size_t fp8attn_kv_tree_workspace_bytes(int rows, int max_q_len, int max_seqlen, 
  * Errors: INVALID (null pointers, negative sizes, num_heads not a multiple of
  * num_kv_heads, a workspace too small, a bad softmax_scale), UNSUPPORTED
  * (head_dim != 128, page_size, strides or alignment, rows > 2048, total_q *
- * num_heads >= 2^31, bounds that allow 2^31 or more 128-key tiles), CUDA.
+ * num_heads >= 2^31, num_heads / num_kv_heads = G > 1024, max_q_len * G * G
+ * close to 2^32, max_seqlen > 2^31 - 256, bounds that allow 2^31 or more
+ * 128-key tiles), CUDA.
  * rows == 0 or total_q == 0 launches nothing. */
 fp8attn_status fp8attn_kv_tree_fwd(const void* q, int64_t q_tok_stride, int64_t q_head_stride,
                                    const void* k_cache, const void* v_cache,

@@ -802,17 +802,17 @@ fp8attn_status fp8attn_kv_tree_fwd(const void* q, int64_t q_tok_stride, int64_t 
   if (max_q_len > total_q) max_q_len = static_cast<int>(total_q);
   const int64_t held = static_cast<int64_t>(table_width) * page_size;
   if (max_seqlen > held) max_seqlen = static_cast<int>(held);
+  // the kernels hold query rows, positions and their ends (a tile further) in
+  // 32 bits, and divide query rows by the group in 32 bits
+  const int64_t group = num_heads / num_kv_heads;
+  if ((max_q_len * group + 128) * group > 0xFFFFFFFFLL || max_q_len * group > 0x7FFFFF00LL ||
+      max_seqlen > 0x7FFFFF00LL ||
+      kv_tree_max_tiles(rows, max_q_len, max_seqlen, num_heads, num_kv_heads) > 0x7FFFFFFFLL)
+    return FP8ATTN_ERR_UNSUPPORTED;
   const size_t need =
       max_q_len && max_seqlen
           ? kv_tree_workspace_bytes(rows, max_q_len, max_seqlen, num_heads, num_kv_heads)
           : 0;
-  // query rows of a KV head are divided by the group in 32 bits
-  const int64_t group = num_heads / num_kv_heads;
-  if ((static_cast<int64_t>(max_q_len) * group + 128) * group > 0xFFFFFFFFLL ||
-      static_cast<int64_t>(max_q_len) * group > 0x7FFFFF00LL)
-    return FP8ATTN_ERR_UNSUPPORTED;
-  if (kv_tree_max_tiles(rows, max_q_len, max_seqlen, num_heads, num_kv_heads) > 0x7FFFFFFFLL)
-    return FP8ATTN_ERR_UNSUPPORTED;
   if (need > workspace_bytes || (need && !workspace)) return FP8ATTN_ERR_INVALID;
   if (!aligned(workspace, 16)) return FP8ATTN_ERR_UNSUPPORTED;
   p.q = q;

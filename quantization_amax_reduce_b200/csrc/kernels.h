@@ -169,7 +169,7 @@ struct KvTreeLaunch {
   int32_t* err;
 };
 
-constexpr int kMaxTreeRows = 2048;    // a prefix sum in shared memory
+constexpr int kMaxTreeRows = 2048;    // every CTA scans all rows
 
 // Work items (128-key tiles of a request's KV heads and query row tiles) that
 // lengths up to the given ones can come to.

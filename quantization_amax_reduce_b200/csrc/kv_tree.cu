@@ -1088,7 +1088,6 @@ bool make_cache_map(CUtensorMap* m, const void* base, const PagedCache& c) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-
 // Query rows of a tile.  Up to 32 rows of a KV head: keys on the lanes, with
 // the fewest columns that hold them (16 is the smallest N); above: rows on the
 // lanes.
@@ -1151,8 +1150,12 @@ cudaError_t launch_t(const KvTreeLaunch& p, const TreeArgs& a, cudaStream_t stre
 
 int64_t kv_tree_max_tiles(int rows, int max_q, int max_seqlen, int heads, int kv_heads) {
   const int R = tile_rows(max_q, heads, kv_heads);
-  const int64_t row_tiles = (static_cast<int64_t>(max_q) * (heads / kv_heads) + R - 1) / R;
-  return row_tiles * kv_heads * rows * ((static_cast<int64_t>(max_seqlen) + kTile - 1) / kTile);
+  // (each factor is below 2^55; a product beyond 2^62 counts as 2^62)
+  int64_t tiles = (static_cast<int64_t>(max_q) * (heads / kv_heads) + R - 1) / R;
+  for (int64_t f : {static_cast<int64_t>(kv_heads), static_cast<int64_t>(rows),
+                    (static_cast<int64_t>(max_seqlen) + kTile - 1) / kTile})
+    tiles = f > 0 && tiles > (int64_t{1} << 62) / f ? int64_t{1} << 62 : tiles * f;
+  return tiles;
 }
 
 size_t kv_tree_workspace_bytes(int rows, int max_q, int max_seqlen, int heads, int kv_heads) {

@@ -93,6 +93,22 @@ def test_tree_refusals(L):
     assert call(f, TREE, total=0, q=None, out=None) == OK
 
 
+def test_tree_sizes_beyond_32_bits(L):
+    f = L.fp8attn_kv_tree_fwd
+    # a tile's end would pass 2^31 (pages may repeat in a table)
+    long = dict(rows=1, kv=32, page=1024, width=1 << 21, max_seq=(1 << 31) - 1, total=1, max_q=1)
+    assert call(f, TREE, **long) == UNSUPPORTED
+    assert call(f, TREE, **dict(long, max_seq=(1 << 31) - 256), ws_bytes=0) == INVALID   # (workspace)
+    # heads x requests x key tiles: 2^30 x 2^11 x (2^24 - 2) tiles
+    assert call(f, TREE, rows=2048, page=1024, width=1 << 21, stride=1 << 21,
+                max_seq=(1 << 31) - 256, total=1, max_q=1, heads=1 << 30,
+                kv=1 << 30) == UNSUPPORTED
+    assert L.fp8attn_kv_tree_workspace_bytes(2048, (1 << 31) - 1, (1 << 31) - 1, (1 << 31) - 1,
+                                             (1 << 31) - 1) > 0
+    for change in (dict(heads=2050, kv=2), dict(heads=1024, kv=1, max_q=1 << 20, total=1 << 20)):
+        assert call(f, TREE, **change) == UNSUPPORTED, change
+
+
 def test_tree_workspace(L):
     f = L.fp8attn_kv_tree_workspace_bytes
     for bad in ((0, 1, 1, 1, 1), (1, 0, 1, 1, 1), (1, 1, 0, 1, 1), (1, 1, 1, 3, 2), (1, 1, 1, 0, 1),
