@@ -608,7 +608,8 @@ size_t fp8attn_kv_tree_workspace_bytes(int rows, int max_q_len, int max_seqlen, 
  * (head_dim != 128, page_size, strides or alignment, rows > 2048, total_q *
  * num_heads >= 2^31, num_heads / num_kv_heads = G > 1024, max_q_len * G * G
  * close to 2^32, max_seqlen > 2^31 - 256, bounds that allow 2^31 or more
- * 128-key tiles), CUDA.
+ * 128-key tiles, counting 4 more for each request's KV heads and query row
+ * tiles), CUDA.
  * rows == 0 or total_q == 0 launches nothing. */
 fp8attn_status fp8attn_kv_tree_fwd(const void* q, int64_t q_tok_stride, int64_t q_head_stride,
                                    const void* k_cache, const void* v_cache,

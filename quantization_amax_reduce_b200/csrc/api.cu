@@ -807,7 +807,7 @@ fp8attn_status fp8attn_kv_tree_fwd(const void* q, int64_t q_tok_stride, int64_t 
   const int64_t group = num_heads / num_kv_heads;
   if ((max_q_len * group + 128) * group > 0xFFFFFFFFLL || max_q_len * group > 0x7FFFFF00LL ||
       max_seqlen > 0x7FFFFF00LL ||
-      kv_tree_max_tiles(rows, max_q_len, max_seqlen, num_heads, num_kv_heads) > 0x7FFFFFFFLL)
+      kv_tree_max_items(rows, max_q_len, max_seqlen, num_heads, num_kv_heads) > 0x7FFFFFFFLL)
     return FP8ATTN_ERR_UNSUPPORTED;
   const size_t need =
       max_q_len && max_seqlen

@@ -171,9 +171,9 @@ struct KvTreeLaunch {
 
 constexpr int kMaxTreeRows = 2048;    // every CTA scans all rows
 
-// Work items (128-key tiles of a request's KV heads and query row tiles) that
-// lengths up to the given ones can come to.
-int64_t kv_tree_max_tiles(int rows, int max_q, int max_seqlen, int heads, int kv_heads);
+// Work items (128-key tiles of a request's KV heads and query row tiles, and a
+// few more for each such unit) that lengths up to the given ones can come to.
+int64_t kv_tree_max_items(int rows, int max_q, int max_seqlen, int heads, int kv_heads);
 size_t kv_tree_workspace_bytes(int rows, int max_q, int max_seqlen, int heads, int kv_heads);
 cudaError_t launch_kv_tree(const KvTreeLaunch& p, cudaStream_t stream);
 

@@ -47,8 +47,9 @@
 // column over 128 lanes.
 //
 // Split: the tiles of all units, in order (request, head, row tile, key tile),
-// are cut into one equal range per CTA, one CTA per SM, so ragged lengths
-// balance without the host knowing them.  A unit that spans CTAs leaves
+// and a few more a unit for what it costs by itself, are cut into one equal
+// range per CTA, one CTA per SM, so ragged lengths balance without the host
+// knowing them.  A unit that spans CTAs leaves
 // (O, ref, sum) of each piece in the workspace, at most two pieces per CTA,
 // and a second kernel joins them in order: results do not depend on timing.
 #include <cuda.h>
@@ -304,7 +305,7 @@ kv_tree_keys_kernel(const __grid_constant__ CUtensorMap tm_k,
       const UnitRows<R>& col = ctl.rows[unit & 3];
       const Segment& seg = col.seg;   // (in shared memory: registers are short)
       if (threadIdx.x == 0 && seg.t0 == 0 && seg.t1 < seg.tiles)
-        a.join[blockIdx.x] = join_info(seg, tiles_per_cta(ctl.chunk[C::kThreads], gridDim.x));
+        a.join[blockIdx.x] = join_info(seg, items_per_cta(ctl.chunk[C::kThreads], gridDim.x));
       const int ctx = seg.seq - seg.n;
       // columns in pairs: row sums of this thread's keys; kPOffset - ref, 0 while unset
       uint64_t sum2[kCols / 2], off2[kCols / 2];
@@ -763,7 +764,7 @@ kv_tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
       const UnitRows<R>& rows = ctl.rows[unit & 3];
       const Segment& seg = rows.seg;   // (in shared memory: registers are short)
       if (threadIdx.x == 0 && seg.t0 == 0 && seg.t1 < seg.tiles)
-        a.join[blockIdx.x] = join_info(seg, tiles_per_cta(ctl.chunk[C::kThreads], gridDim.x));
+        a.join[blockIdx.x] = join_info(seg, items_per_cta(ctl.chunk[C::kThreads], gridDim.x));
       const int ctx = seg.seq - seg.n;
       const float factor = rows.factor[row];
       const int node = rows.node[row];
@@ -1097,8 +1098,8 @@ int tile_rows(int max_q, int heads, int kv_heads) {
 }
 
 int launch_ctas(int rows, int max_q, int max_seqlen, int heads, int kv_heads) {
-  const int64_t tiles = kv_tree_max_tiles(rows, max_q, max_seqlen, heads, kv_heads);
-  const int64_t ctas = (tiles + kMinTiles - 1) / kMinTiles;
+  const int64_t items = kv_tree_max_items(rows, max_q, max_seqlen, heads, kv_heads);
+  const int64_t ctas = (items + kMinItems - 1) / kMinItems;
   return static_cast<int>(ctas < 1 ? 1 : ctas < kMaxCtas ? ctas : kMaxCtas);
 }
 
@@ -1148,14 +1149,15 @@ cudaError_t launch_t(const KvTreeLaunch& p, const TreeArgs& a, cudaStream_t stre
 
 }  // namespace
 
-int64_t kv_tree_max_tiles(int rows, int max_q, int max_seqlen, int heads, int kv_heads) {
+int64_t kv_tree_max_items(int rows, int max_q, int max_seqlen, int heads, int kv_heads) {
   const int R = tile_rows(max_q, heads, kv_heads);
-  // (each factor is below 2^55; a product beyond 2^62 counts as 2^62)
-  int64_t tiles = (static_cast<int64_t>(max_q) * (heads / kv_heads) + R - 1) / R;
+  const int64_t tiles = (static_cast<int64_t>(max_seqlen) + kTile - 1) / kTile;
+  // (each factor is below 2^31; a product beyond 2^62 counts as 2^62)
+  int64_t items = (static_cast<int64_t>(max_q) * (heads / kv_heads) + R - 1) / R;
   for (int64_t f : {static_cast<int64_t>(kv_heads), static_cast<int64_t>(rows),
-                    (static_cast<int64_t>(max_seqlen) + kTile - 1) / kTile})
-    tiles = f > 0 && tiles > (int64_t{1} << 62) / f ? int64_t{1} << 62 : tiles * f;
-  return tiles;
+                    tiles > 0 ? kUnitCost + tiles : 0})
+    items = f > 0 && items > (int64_t{1} << 62) / f ? int64_t{1} << 62 : items * f;
+  return items;
 }
 
 size_t kv_tree_workspace_bytes(int rows, int max_q, int max_seqlen, int heads, int kv_heads) {

@@ -21,10 +21,16 @@ constexpr int kTile = 128;                 // keys of a tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kPOffset = 8.0f;           // log2 of P at the reference
 constexpr float kRefLag = 7.0f;
-// A CTA's range is at least this many tiles: below it another CTA and the
+// A CTA's range is at least this many items: below it another CTA and the
 // join of its piece cost more than the tiles they save.
-constexpr int kMinTiles = 4;
+constexpr int kMinItems = 4;
 constexpr int kMaxCtas = 148;              // one per SM
+// What a unit costs beside its tiles (its Q, the way through the pipeline, its
+// epilogue), in tiles: ranges are cut by tiles plus this, or a CTA whose
+// requests are short works through a dozen units while others read one long
+// one.  128 chains of 4 over 5 to 300 tokens: 73 us at 0, 60 at 2, 58 at 4, 63
+// at 10; 16 trees of up to 25 over 100 to 5000 tokens (bf16): 81, 56, 49, 53.
+constexpr int kUnitCost = 4;
 constexpr int kPrepWarps = 4, kPrepThreads = 32 * kPrepWarps;
 
 struct TreeArgs {
@@ -158,7 +164,9 @@ __device__ __forceinline__ uint32_t low_bits(int n) {   // the n lowest bits, 0 
 }
 
 // ---------------------------------------------------------------------------
-// Work list: every role walks the same segments (a CTA's tiles of one unit).
+// Work list: the units in order (request, head, row tile), each kUnitCost items
+// and then an item per tile, cut into a range of items per CTA.  Every role
+// walks the same segments (a CTA's tiles of one unit).
 // ---------------------------------------------------------------------------
 
 // Node of a query row: row / group, exact while row * group < 2^32.
@@ -168,7 +176,8 @@ __device__ __forceinline__ int node_of(const TreeArgs& a, int row) {
 
 struct Request {
   int seq, q0, n, tiles, row_tiles;
-  __device__ __forceinline__ int work(int kv_heads) const { return kv_heads * row_tiles * tiles; }
+  int span;              // items of a unit: its cost and its tiles
+  __device__ __forceinline__ int work(int kv_heads) const { return kv_heads * row_tiles * span; }
 };
 
 // A request's lengths; false if they are inconsistent (it then has no work).
@@ -184,10 +193,11 @@ __device__ __forceinline__ bool read_request(const TreeArgs& a, int b, Request& 
                   (!a.mask || r.n <= 64ll * a.mask_words);
   r.tiles = ok ? (r.seq + kTile - 1) / kTile : 0;
   r.row_tiles = ok ? (r.n * a.group + R - 1) / R : 0;
+  r.span = kUnitCost + r.tiles;
   return ok;
 }
 
-// chunk[i] = tiles of the requests before thread i's; chunk[kThreads] = all.
+// chunk[i] = items of the requests before thread i's; chunk[kThreads] = all.
 // Returns whether this thread met an inconsistent request.
 template <int R, int kThreads>
 __device__ bool scan_requests(const TreeArgs& a, int* chunk, int* warp_sums) {
@@ -255,9 +265,9 @@ struct Finder {
   }
 };
 
-// Tiles of a CTA's range.
-__device__ __forceinline__ int tiles_per_cta(int total, int ctas) {
-  return max(kMinTiles, (total + ctas - 1) / ctas);
+// Items of a CTA's range.
+__device__ __forceinline__ int items_per_cta(int total, int ctas) {
+  return max(kMinItems, (total + ctas - 1) / ctas);
 }
 
 // The pieces of a unit that begins with `s`, which its CTA does not finish.
@@ -272,7 +282,7 @@ struct Walker {
   int head = 0, rt = -1;     // the unit handed out last (its last tile was, too)
   __device__ __forceinline__ void init(const int* chunk, int ctas) {
     const int total = chunk[kThreads];
-    const int per = tiles_per_cta(total, ctas);
+    const int per = items_per_cta(total, ctas);
     const int64_t from = static_cast<int64_t>(blockIdx.x) * per;
     w = static_cast<int>(min(from, static_cast<int64_t>(total)));
     end = static_cast<int>(min(from + per, static_cast<int64_t>(total)));
@@ -284,13 +294,13 @@ struct Walker {
     const int old = find.b;
     find.seek(a, chunk, w);
     const Request& r = find.r;
-    s.t0 = 0;
+    int x0 = 0;
     if (first) {             // somewhere inside a unit
       const int local = w - find.start;
-      const int unit = local / r.tiles;
+      const int unit = local / r.span;
       head = unit / r.row_tiles;
       rt = unit - head * r.row_tiles;
-      s.t0 = local - unit * r.tiles;
+      x0 = local - unit * r.span;
     } else if (find.b != old) {
       head = rt = 0;
     } else if (++rt == r.row_tiles) {
@@ -304,9 +314,11 @@ struct Walker {
     s.tiles = r.tiles;
     s.head = head;
     s.rt = rt;
-    s.t1 = min(s.tiles, s.t0 + (end - w));
-    w += s.t1 - s.t0;
-    return true;
+    const int x1 = min(r.span, x0 + (end - w));
+    w += x1 - x0;
+    s.t0 = max(0, x0 - kUnitCost);
+    s.t1 = max(0, x1 - kUnitCost);
+    return s.t1 > 0;         // (none: the range ends before the unit's first tile)
   }
 };
 
