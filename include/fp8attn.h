@@ -602,7 +602,7 @@ size_t fp8attn_kv_tree_workspace_bytes(int rows, int max_q_len, int max_seqlen, 
  * below n_b, above max_seqlen or beyond table_width pages, queries beyond
  * total_q, or more than 64 mask_words nodes: it is left out, its rows stay as
  * they are), PAGES (a page id outside the cache: its keys and values are read
- * as zeros), TIMEOUT.
+ * as zeros), TIMEOUT (out is then undefined).
  * Errors: INVALID (null pointers, negative sizes, num_heads not a multiple of
  * num_kv_heads, a workspace too small, a bad softmax_scale), UNSUPPORTED
  * (head_dim != 128, page_size, strides or alignment, rows > 2048, total_q *

@@ -301,7 +301,8 @@ kv_tree_keys_kernel(const __grid_constant__ CUtensorMap tm_k,
     const float ds_v = kFp8 ? __ldg(a.descale + 2) : 1.0f;
     if (threadIdx.x == 0 && a.join) a.join[blockIdx.x] = {0, 0, 0, 0, 0};
     int g = 0;
-    for (int unit = 0; unit_at(unit); ++unit) {
+    // (all softmax warps share barriers in a unit: they agree to begin it)
+    for (int unit = 0; !group_any(1 + C::kGroups, C::kSoftmaxThreads, !unit_at(unit)); ++unit) {
       const UnitRows<R>& col = ctl.rows[unit & 3];
       const Segment& seg = col.seg;   // (in shared memory: registers are short)
       if (threadIdx.x == 0 && seg.t0 == 0 && seg.t1 < seg.tiles)
@@ -389,7 +390,7 @@ kv_tree_keys_kernel(const __grid_constant__ CUtensorMap tm_k,
         }
 
         // ---- does the reference of a column move?
-        if (group_any(bar_wg, unset != 0 || top > kPOffset + kRefLag)) {
+        if (group_any(bar_wg, 128, unset != 0 || top > kPOffset + kRefLag)) {
           float v[kCols];
 #pragma unroll
           for (int c = 0; c < kCols; ++c) v[c] = x[c];
@@ -760,7 +761,7 @@ kv_tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
     const float ds_v = kFp8 ? __ldg(a.descale + 2) : 1.0f;
     if (threadIdx.x == 0 && a.join) a.join[blockIdx.x] = {0, 0, 0, 0, 0};
     int g = 0;
-    for (int unit = 0; unit_at(unit); ++unit) {
+    for (int unit = 0; !group_any(1, C::kSoftmaxThreads, !unit_at(unit)); ++unit) {
       const UnitRows<R>& rows = ctl.rows[unit & 3];
       const Segment& seg = rows.seg;   // (in shared memory: registers are short)
       if (threadIdx.x == 0 && seg.t0 == 0 && seg.t1 < seg.tiles)

@@ -89,16 +89,16 @@ __device__ __forceinline__ void group_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// Does any of the group's 128 threads say yes?
-__device__ __forceinline__ bool group_any(int id, bool yes) {
+// Does any of the group's threads say yes?
+__device__ __forceinline__ bool group_any(int id, int threads, bool yes) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 q, %1, 0;\n\t"
-      "bar.red.or.pred p, %2, 128, q;\n\t"
+      "bar.red.or.pred p, %2, %3, q;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}\n"
       : "=r"(r)
-      : "r"(static_cast<uint32_t>(yes)), "r"(id)
+      : "r"(static_cast<uint32_t>(yes)), "r"(id), "r"(threads)
       : "memory");
   return r != 0;
 }
@@ -324,8 +324,10 @@ struct Walker {
 
 // ---------------------------------------------------------------------------
 // Waits.  One that gives up sets the abort flag, which ends all other waits at
-// once; the roles then run on without data (so that every barrier is met) and
-// write no output.  (The whole warp tests: 64 cycles when the phase is over
+// once.  Warps that share a barrier must still agree on what comes next: the
+// preparing warps go through all of their units, but hand out no more of them,
+// and the softmax warps run on without data to the end of their unit, where
+// they vote on whether there is a next one.  Nothing is written out then.  (The whole warp tests: 64 cycles when the phase is over
 // already, against 117 for one lane and a warp sync.)
 // ---------------------------------------------------------------------------
 
@@ -488,7 +490,7 @@ __device__ __forceinline__ void split_q(uint4 x, int e, bool whole, uint8_t* sq,
 template <int R, bool kFp8, int kLoScale>
 __device__ __forceinline__ void store_q(const TreeArgs& a, const Segment& s, QLoads<R>& q,
                                         uint8_t* sq, UnitRows<R>& rows, uint2* row_max,
-                                        int barrier, float unit_factor, int tid) {
+                                        int barrier, float unit_factor, int tid, bool hand_out) {
   constexpr int kLoads = QLoads<R>::kLoads, kRows = QLoads<R>::kRows, kAll = QLoads<R>::kAll;
   const int c = tid & 15, lane = tid & 31;
   // a row with Inf or NaN becomes NaN throughout (E4M3)
@@ -545,14 +547,14 @@ __device__ __forceinline__ void store_q(const TreeArgs& a, const Segment& s, QLo
     if (!kFp8 && tid < R) rows.factor[tid] = unit_factor;
     if (!kFp8 && tid == 0) rows.one_factor = 1;
   }
-  if (tid < R) {
+  if (tid < R && hand_out) {
     const int row = s.rt * R + (is_doubled<R>(a, s) ? tid & 63 : tid);
     const int node = node_of(a, row), gq = row - node * a.group;
     const bool live = node < s.n;
     rows.node[tid] = live ? node : -1;
     rows.out_row[tid] = live ? (s.q0 + node) * (a.kv_heads * a.group) + s.head * a.group + gq : -1;
   }
-  if (tid == 0) rows.seg = s;
+  if (tid == 0 && hand_out) rows.seg = s;
   fence_proxy_async();
 }
 
@@ -682,11 +684,14 @@ __device__ __forceinline__ void prepare(const TreeArgs& a, const Waits& w, const
   for (int unit = 0;; ++unit) {
     seg = next;
     if (g > 0) s_done(g - 1);
+    // (after an abort somebody may still use the unit that lies there)
+    const bool hand_out = !w.aborted();
     if (more)
-      store_q<R, kFp8, kLoScale>(a, seg, q, sq, rows[unit & 3], row_max, barrier, unit_factor, tid);
-    else if (tid == 0)
+      store_q<R, kFp8, kLoScale>(a, seg, q, sq, rows[unit & 3], row_max, barrier, unit_factor, tid,
+                                 hand_out);
+    else if (tid == 0 && hand_out)
       rows[unit & 3].seg.t0 = rows[unit & 3].seg.t1 = 0;
-    w.arrive(&q_full[unit & 1]);
+    if (hand_out) w.arrive(&q_full[unit & 1]);
     if (!more) return;
     more = walk.next(a, chunk, next);
     if (more) q.load(a, next, tid, 0);
