@@ -572,8 +572,10 @@ __device__ __forceinline__ void store_q(const TreeArgs& a, const Segment& s, QLo
 // i & 1, of a row of the eight from 32 warp + 8 (i / 2) on.  It becomes pieces
 // 2 (lane & 3) and + 1 of half h.  Of the eight lanes that share a bank cycle
 // four have row p and four row p ^ 5: bit 2 apart their reads, bit 0 apart
-// their writes fall into different banks.  `taken` runs when the source is
-// read, `ready` before the destination is written.
+// their writes fall into different banks.  `ready` runs before the destination
+// is written, `taken` when the source may be overwritten: behind the proxy
+// fence, since TMA will (an arrival right behind the loads was seen to overtake
+// the last of them).
 template <int kBatch, class Taken, class Ready>
 __device__ __forceinline__ bool widen_v(const uint8_t* src, uint8_t* wide, int tid, bool tail,
                                         int pos0, int ctx, int seq, Taken taken, Ready ready) {
@@ -590,7 +592,6 @@ __device__ __forceinline__ bool widen_v(const uint8_t* src, uint8_t* wide, int t
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
       x[i] = *reinterpret_cast<const uint4*>(from + (i0 + i) / 2 * 1024 + (i & 1 ? f1 : f0));
-    if (i0 + kBatch == 8) taken();
     if (tail) {
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
@@ -620,6 +621,7 @@ __device__ __forceinline__ bool widen_v(const uint8_t* src, uint8_t* wide, int t
     }
   }
   fence_proxy_async();
+  taken();
   return wild;
 }
 
