@@ -114,7 +114,7 @@ struct AssignPagesLaunch {
   int32_t* err;
 };
 
-constexpr int kMaxPageRows = 16384;   // three prefix sums in shared memory
+constexpr int kMaxPageRows = 16384;   // three prefix sums of 4 bytes a row in shared memory
 
 cudaError_t launch_assign_pages(const AssignPagesLaunch& p, cudaStream_t stream);
 
