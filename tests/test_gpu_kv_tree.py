@@ -400,6 +400,60 @@ def test_same_bits_over_many_runs(nodes, hq, hkv, length, fp8):
 
 
 
+@pytest.mark.parametrize("fp8", [True, False])
+def test_requests_that_share_pages(fp8):
+    """A common prompt lies in the cache once; one request appears twice."""
+    s = make(33, [300, 300, 300, 260], [9, 9, 9, 1], 8, 2, 16, fp8)
+    s["tables"][1, :17] = s["tables"][0, :17]      # 272 of the 291 tokens of context
+    s["tables"][2] = s["tables"][0]
+    s["tables"][3, :16] = s["tables"][0, :16]
+    check(run(s), *expect(s))
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("nodes", [1, 2])
+def test_a_thousand_query_heads_to_a_kv_head(nodes, fp8):
+    s = make(34, [400, nodes], [nodes, nodes], 1024, 1, 32, fp8)
+    check(run(s), *expect(s))
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+def test_mask_bits_beyond_the_nodes_are_ignored(fp8):
+    s = make(35, [200, 90, 64], [5, 64, 33], 4, 2, 16, fp8)
+    want = run(s)
+    for b in range(3):
+        n = int(s["cu"][b + 1] - s["cu"][b])
+        if n < 64:
+            s["mask"][s["cu"][b]:s["cu"][b + 1], 0] |= np.uint64((1 << 64) - (1 << n))
+    assert torch.equal(run(s), want)
+
+
+def test_two_graphs_replayed_side_by_side():
+    """Each graph has its own workspace, whatever the other one does meanwhile."""
+    sets = [to_dev(make(36, [5000, 700, 3000], [2, 2, 1], 16, 2, 64, True)),
+            to_dev(make(37, [4000, 2500], [40, 64], 16, 4, 16, False))]
+    want = [qar.kv_tree_fwd(*a) for a in sets]
+    outs = [torch.empty_like(w) for w in want]
+    graphs, streams = [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for a, out in zip(sets, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(5):
+                qar.kv_tree_fwd(*a, out=out)
+        graphs.append(g)
+    for _ in range(20):
+        for out in outs:
+            out.zero_()
+        torch.cuda.synchronize()
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+        for out, w in zip(outs, want):
+            assert torch.equal(out, w)
+
+
+
 def test_empty_calls():
     s = make(2, [40], [4], 4, 2, 16, False)
     a = to_dev(s)
