@@ -17,6 +17,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
+import importlib
 import math
 import os
 from typing import Dict, Iterable, List, Optional, Sequence, Tuple
@@ -583,19 +584,30 @@ def _launch_on(stream, device):
 
 
 # (These calls take microseconds on the device, so their checks are lean: types
-# are compared by identity, sizes and strides read once.)
+# are compared by identity, sizes and strides read once, int32 tensors and the
+# calls themselves go through a CPython module.)
 _I32, _I64, _U8, _BF16, _F32 = (torch.int32, torch.int64, torch.uint8, torch.bfloat16,
                                 torch.float32)
 
 
-def _int32(t, name: str, device, numel: int = -1) -> int:
-    """Pointer of a contiguous int32 tensor on ``device`` (of ``numel`` elements)."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not _I32 or t.device != device:
-        raise ValueError(f"{name} must be an int32 tensor on {device}")
-    if not t.is_contiguous() or (numel >= 0 and t.numel() != numel):
-        raise ValueError(f"{name} must be contiguous" +
-                         (f" and hold {numel} elements" if numel >= 0 else ""))
-    return t.data_ptr()
+_native_calls = None
+
+
+def _native():
+    """The CPython calls of the entry points below (csrc/calls.c)."""
+    global _native_calls
+    if _native_calls is None:
+        L = lib()
+        try:
+            module = importlib.import_module("._calls", __name__)
+        except ImportError as e:
+            raise RuntimeError("the _calls module is missing: build it with "
+                               "`python -m quantization_amax_reduce_b200.build`") from e
+        entries = (L.fp8attn_kv_assign_pages, L.fp8attn_kv_write, L.fp8attn_kv_tree_fwd,
+                   L.fp8attn_kv_keep_path)
+        module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in entries), torch.Tensor, _I32)
+        _native_calls = module
+    return _native_calls
 
 
 def _table(t, name: str, rows: int, device, least: int = 0):
@@ -645,8 +657,8 @@ def _scale3(scale, name: str, fp8: bool, device) -> int:
     return int(scale)
 
 
-def _error_ptr(error, device) -> int:
-    return 0 if error is None else _int32(error, "error", device, 1)
+def _error_ptr(C, error, device: int) -> int:
+    return 0 if error is None else C.int32_ptr(error, "error", device, 1)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -674,12 +686,14 @@ def kv_assign_pages(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_tables
     fp8attn_kv_assign_pages in fp8attn.h)."""
     _require_cuda(seq_lens, "seq_lens")
     dev, rows, max_tokens = seq_lens.device, seq_lens.numel(), int(max_tokens)
+    C, at = _native(), dev.index
     if max_tokens < 0:
         raise ValueError("max_tokens must not be negative")
     tables, table_stride, width = _table(block_tables, "block_tables", rows, dev, 1)
-    seq, new = _int32(seq_lens, "seq_lens", dev), _int32(new_lens, "new_lens", dev, rows)
-    own, free = _int32(owned, "owned", dev, rows), _int32(free_pages, "free_pages", dev)
-    count, err = _int32(pool, "pool", dev, 2), _error_ptr(error, dev)
+    int32 = C.int32_ptr
+    seq, new = int32(seq_lens, "seq_lens", at, -1), int32(new_lens, "new_lens", at, rows)
+    own, free = int32(owned, "owned", at, rows), int32(free_pages, "free_pages", at, -1)
+    count, err = int32(pool, "pool", at, 2), _error_ptr(C, error, at)
     handle, on = _launch_on(stream, dev)
     with on:
         if out is None:
@@ -693,7 +707,7 @@ def kv_assign_pages(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_tables
             _check_out(positions, "positions", _I32, max_tokens, dev)
         if rows == 0:
             cu.zero_()
-        status = lib().fp8attn_kv_assign_pages(
+        status = C.assign_pages(
             seq, new, rows, int(page_size), tables, table_stride, width, own, free,
             free_pages.numel(), count, max_tokens, cu.data_ptr(), slots.data_ptr(),
             positions.data_ptr(), err, handle)
@@ -712,6 +726,7 @@ def kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: tor
     ``Context.static_quant_scale_ptr(layer)``) or a 3-element fp32 tensor
     {qs_q, qs_k, qs_v}; bf16 caches take no scale."""
     pages, page_size, heads, strides, fp8, dev = _paged_cache(k_cache, v_cache)
+    C, at = _native(), dev.index
     for name, t in (("k", k), ("v", v)):
         _require_cuda(t, name)
         if t.dtype is not _BF16 or t.device != dev:
@@ -725,13 +740,13 @@ def kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: tor
     if not isinstance(slots, torch.Tensor) or slots.dtype is not _I64 or \
             slots.device != dev or slots.shape != (T,) or not slots.is_contiguous():
         raise ValueError(f"slots must be a contiguous int64 [{T}] tensor on {dev}")
-    scale, err = _scale3(quant_scale, "quant_scale", fp8, dev), _error_ptr(error, dev)
+    scale, err = _scale3(quant_scale, "quant_scale", fp8, dev), _error_ptr(C, error, at)
     # the stride of a dimension of size one says nothing
     tok_stride = steps[0] if T > 1 else heads * HEAD_DIM
     head_stride = steps[1] if heads > 1 else HEAD_DIM
     handle, on = _launch_on(stream, dev)
     with on:
-        status = lib().fp8attn_kv_write(
+        status = C.write(
             k.data_ptr(), v.data_ptr(), tok_stride, head_stride, slots.data_ptr(), T, heads,
             HEAD_DIM, k_cache.data_ptr(), v_cache.data_ptr(), strides[0], strides[1], strides[2],
             pages, page_size, scale, err, handle)
@@ -758,6 +773,7 @@ def kv_tree_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     bf16 cache takes none.  Returns bf16 [T, heads, 128] (a query that sees
     nothing: 0; rows of no request in a given ``out`` stay as they are)."""
     pages, page_size, kv_heads, strides, fp8, dev = _paged_cache(k_cache, v_cache)
+    C, at = _native(), dev.index
     _require_cuda(q, "q")
     if q.dtype is not _BF16 or q.device != dev:
         raise ValueError(f"q must be bfloat16 on {dev}")
@@ -770,7 +786,7 @@ def kv_tree_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     _require_cuda(seq_lens, "seq_lens")
     rows = seq_lens.numel()
     tables, table_stride, width = _table(block_tables, "block_tables", rows, dev, 1)
-    seq, cu = _int32(seq_lens, "seq_lens", dev), _int32(cu_q, "cu_q", dev, rows + 1)
+    seq, cu = C.int32_ptr(seq_lens, "seq_lens", at, -1), C.int32_ptr(cu_q, "cu_q", at, rows + 1)
     mask = words = 0
     if tree_mask is not None:
         if not isinstance(tree_mask, torch.Tensor) or tree_mask.dtype is not _I64 or \
@@ -778,7 +794,7 @@ def kv_tree_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                 tree_mask.shape[1] < 1 or not tree_mask.is_contiguous():
             raise ValueError(f"tree_mask must be a contiguous int64 [{T}, words] tensor on {dev}")
         mask, words = tree_mask.data_ptr(), tree_mask.shape[1]
-    scale, err = _scale3(descale, "descale", fp8, dev), _error_ptr(error, dev)
+    scale, err = _scale3(descale, "descale", fp8, dev), _error_ptr(C, error, at)
     tok_stride = steps[0] if T > 1 else heads * HEAD_DIM
     head_stride = steps[1] if heads > 1 else HEAD_DIM
     max_q_len, max_seqlen = int(max_q_len), int(max_seqlen)
@@ -790,7 +806,7 @@ def kv_tree_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
         else:
             _check_out(out, "out", _BF16, T * heads * HEAD_DIM, dev)
         work = seq_lens.new_empty(need) if need else None
-        status = lib().fp8attn_kv_tree_fwd(
+        status = C.tree_fwd(
             q.data_ptr(), tok_stride, head_stride, k_cache.data_ptr(), v_cache.data_ptr(),
             strides[0], strides[1], strides[2], pages, page_size, tables, table_stride, width,
             seq, cu, rows, max_q_len, max_seqlen, T, heads, kv_heads, HEAD_DIM, scale, mask,
@@ -811,15 +827,16 @@ def kv_keep_path(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: tor
     positions, move to nodes 0, 1, ... of the cache, in place.  The request
     then holds seq_lens[b] - n_b + keep_lens[b] tokens."""
     pages, page_size, heads, strides, _, dev = _paged_cache(k_cache, v_cache)
+    C, at = _native(), dev.index
     _require_cuda(seq_lens, "seq_lens")
     rows = seq_lens.numel()
     tables, table_stride, width = _table(block_tables, "block_tables", rows, dev, 1)
     path, path_stride, depth = _table(paths, "paths", rows, dev)
-    seq, cu = _int32(seq_lens, "seq_lens", dev), _int32(cu_q, "cu_q", dev, rows + 1)
-    keep, err = _int32(keep_lens, "keep_lens", dev, rows), _error_ptr(error, dev)
+    seq, cu = C.int32_ptr(seq_lens, "seq_lens", at, -1), C.int32_ptr(cu_q, "cu_q", at, rows + 1)
+    keep, err = C.int32_ptr(keep_lens, "keep_lens", at, rows), _error_ptr(C, error, at)
     handle, on = _launch_on(stream, dev)
     with on:
-        status = lib().fp8attn_kv_keep_path(
+        status = C.keep_path(
             k_cache.data_ptr(), v_cache.data_ptr(), strides[0], strides[1], strides[2], pages,
             page_size, k_cache.element_size(), heads, HEAD_DIM, tables, table_stride, width, seq,
             cu, rows, path, path_stride, depth, keep, err, handle)

@@ -1,4 +1,6 @@
-"""Build ``libfp8attn.so`` in-tree with nvcc for sm_100a (B200).
+"""Build ``libfp8attn.so`` in-tree with nvcc for sm_100a (B200), and beside it
+the small CPython module ``_calls`` (gcc) through which the binding makes the
+calls that take only microseconds.
 
     python -m quantization_amax_reduce_b200.build [--force] [--verbose]
 
@@ -11,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -19,6 +22,8 @@ SOURCES = ["api.cu", "quant.cu", "attention.cu", "regroup.cu", "scale_map.cu",
            "kv_cache.cu", "kv_tree.cu"]
 HEADERS = ["kernels.h", "kv_tree.cuh", "sm100_ptx.cuh", "state.cuh"]
 LIB = os.path.join(HERE, "libfp8attn.so")
+CALLS_SRC = os.path.join(CSRC, "calls.c")
+CALLS = os.path.join(HERE, "_calls" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -29,16 +34,31 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
+def _older(target: str, deps) -> bool:
+    return not os.path.exists(target) or \
+        any(os.path.getmtime(d) > os.path.getmtime(target) for d in deps)
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB):
-        return True
-    t = os.path.getmtime(LIB)
     deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
-    deps.append(os.path.join(ROOT, "include", "fp8attn.h"))
-    return any(os.path.getmtime(d) > t for d in deps)
+    return _older(LIB, deps + [os.path.join(ROOT, "include", "fp8attn.h")])
+
+
+def _build_calls(force: bool) -> None:
+    if not force and not _older(CALLS, [CALLS_SRC, os.path.join(ROOT, "include", "fp8attn.h")]):
+        return
+    cc = os.environ.get("CC") or shutil.which("gcc") or shutil.which("cc")
+    if not cc:
+        raise RuntimeError("no C compiler found")
+    tmp = CALLS + ".tmp"
+    subprocess.check_call([cc, "-O2", "-shared", "-fPIC", "-Wall", "-I",
+                           sysconfig.get_paths()["include"], "-I", os.path.join(ROOT, "include"),
+                           CALLS_SRC, "-o", tmp])
+    os.replace(tmp, CALLS)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    _build_calls(force)
     if not force and not _stale():
         return LIB
     objdir = os.path.join(ROOT, "_build")

@@ -162,6 +162,46 @@ def test_python_refuses_host_tensors():
         qar.kv_keep_path(c, c, i, i, i, i, i)
 
 
+def test_native_calls_pass_their_arguments_on(L):
+    """The CPython calls give the entry points' own answers, argument for
+    argument, and refuse what these would not see."""
+    import quantization_amax_reduce_b200 as qar
+    C = qar._native()
+    plain = lambda d: [x.value or 0 if isinstance(x, P) else 0 if x is None else x  # noqa: E731
+                       for x in d.values()]
+    assert C.write(*plain(dict(WRITE, tokens=0))) == OK
+    assert C.tree_fwd(*plain(dict(TREE, rows=0))) == OK
+    for k, v, status in (("dim", 64, UNSUPPORTED), ("page", 12, UNSUPPORTED), ("num", 0, INVALID),
+                         ("heads", 0, INVALID), ("slot_stride", 64, UNSUPPORTED), ("k", P(8), UNSUPPORTED),
+                         ("slots", None, INVALID), ("chead", 136, UNSUPPORTED)):
+        assert C.write(*plain(dict(WRITE, **{k: v}))) == status, k
+    for k, v, status in (("scale", float("nan"), INVALID), ("words", 0, INVALID), ("qt", 4100, UNSUPPORTED),
+                         ("width", 0, INVALID), ("rows", 2049, UNSUPPORTED), ("ws", P(8), UNSUPPORTED),
+                         ("out", P(8), UNSUPPORTED), ("kv", 0, INVALID), ("stride", 7, INVALID)):
+        assert C.tree_fwd(*plain(dict(TREE, **{k: v}))) == status, k
+    for call, good in ((C.write, WRITE), (C.tree_fwd, TREE)):
+        with pytest.raises(TypeError, match="number of arguments"):
+            call(*plain(good)[:-1])
+        with pytest.raises(TypeError, match="number of arguments"):
+            call(*plain(good), 0)
+        with pytest.raises(ValueError, match="fit an int"):
+            call(*plain(dict(good, num=1 << 40)))
+        with pytest.raises(TypeError):
+            call(*plain(dict(good, num="16")))
+    with pytest.raises(ValueError, match="x must be an int32 tensor on cuda:0"):
+        C.int32_ptr([1], "x", 0, -1)
+    t = torch.zeros(4, 6, dtype=torch.int32)   # (a host tensor is on device -1)
+    with pytest.raises(ValueError, match="x must be an int32 tensor on cuda:0"):
+        C.int32_ptr(t, "x", 0, -1)
+    with pytest.raises(ValueError, match="int32"):
+        C.int32_ptr(t.long(), "x", -1, -1)
+    with pytest.raises(ValueError, match="x must be contiguous and hold 5 elements"):
+        C.int32_ptr(t, "x", -1, 5)
+    with pytest.raises(ValueError, match="x must be contiguous$"):
+        C.int32_ptr(t.t(), "x", -1, -1)
+    assert C.int32_ptr(t[2:], "x", -1, 12) == t.data_ptr() + 48
+
+
 def test_reference_pool_restores_its_list():
     """The definition's own property: taking pages and giving the same ones
     back leaves the free list as it was (mixed growth and shrinkage between)."""
