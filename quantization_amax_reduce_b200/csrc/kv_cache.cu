@@ -285,8 +285,9 @@ __global__ void __launch_bounds__(kPagesThreads) assign_pages_kernel(const Pages
 // or 8 (bf16) of K and the same of V; the lanes of a (token, head) row are
 // neighbours, so loads and stores are whole 128-byte lines in both page
 // layouts.  Bound: HBM (3 bytes a value for E4M3, 4 for bf16): 8075 tokens of 16
-// heads from a fused QKV projection 13.9 us from cold caches, 99 MB, 7.1 TB/s
-// with part of the writes still in L2; 64 tokens of 8 heads 2.0 us (launch).
+// heads from a fused QKV projection, 99 MB, 17.1 us from and to cold memory (5.8
+// TB/s; 18.1 with 8 resident CTAs an SM that loop), 12.5 us where the buffers
+// stay in L2; 64 tokens of 8 heads 2.0 us (launch).
 // ---------------------------------------------------------------------------
 
 constexpr int kWriteThreads = 256;
@@ -330,38 +331,37 @@ __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(const WriteArgs
   constexpr int kRowsPerCta = kWriteThreads / kLanes;
   const int c = (threadIdx.x % kLanes) * kChannels;
   const float qs_k = kFp8 ? __ldg(a.qs + 1) : 0.0f, qs_v = kFp8 ? __ldg(a.qs + 2) : 0.0f;
-  for (uint64_t r = static_cast<uint64_t>(blockIdx.x) * kRowsPerCta + threadIdx.x / kLanes;
-       r < a.rows; r += static_cast<uint64_t>(gridDim.x) * kRowsPerCta) {
-    const uint32_t t = static_cast<uint32_t>(r) / static_cast<uint32_t>(a.heads);
-    const uint32_t h = static_cast<uint32_t>(r) - t * static_cast<uint32_t>(a.heads);
-    const int64_t slot = __ldg(reinterpret_cast<const long long*>(a.slots) + t);
-    const int64_t from = static_cast<int64_t>(t) * a.tok_stride + h * a.head_stride + c;
-    const uint16_t* k = a.src[0] + from;
-    const uint16_t* v = a.src[1] + from;
-    // the loads do not wait for the slot
-    const uint4 k0 = ld_stream(k), v0 = ld_stream(v);
-    uint4 k1 = make_uint4(0, 0, 0, 0), v1 = k1;
-    if (kFp8) {
-      k1 = ld_stream(k + 8);
-      v1 = ld_stream(v + 8);
-    }
-    if (slot < 0) continue;
-    if (slot >= a.num_slots) {
-      raise_error(a.err, kErrPages);
-      continue;
-    }
-    const int64_t to = (slot >> a.page_log2) * a.page_stride +
-                       (slot & ((1 << a.page_log2) - 1)) * a.slot_stride +
-                       h * a.cache_head_stride + c;
-    if (kFp8) {
-      const uint2 ka = cast8(k0, qs_k), kb = cast8(k1, qs_k);
-      const uint2 va = cast8(v0, qs_v), vb = cast8(v1, qs_v);
-      *reinterpret_cast<uint4*>(a.dst[0] + to) = make_uint4(ka.x, ka.y, kb.x, kb.y);
-      *reinterpret_cast<uint4*>(a.dst[1] + to) = make_uint4(va.x, va.y, vb.x, vb.y);
-    } else {
-      *reinterpret_cast<uint4*>(a.dst[0] + 2 * to) = k0;
-      *reinterpret_cast<uint4*>(a.dst[1] + 2 * to) = v0;
-    }
+  const uint64_t r = static_cast<uint64_t>(blockIdx.x) * kRowsPerCta + threadIdx.x / kLanes;
+  if (r >= a.rows) return;
+  const uint32_t t = static_cast<uint32_t>(r) / static_cast<uint32_t>(a.heads);
+  const uint32_t h = static_cast<uint32_t>(r) - t * static_cast<uint32_t>(a.heads);
+  const int64_t slot = __ldg(reinterpret_cast<const long long*>(a.slots) + t);
+  const int64_t from = static_cast<int64_t>(t) * a.tok_stride + h * a.head_stride + c;
+  const uint16_t* k = a.src[0] + from;
+  const uint16_t* v = a.src[1] + from;
+  // the loads do not wait for the slot
+  const uint4 k0 = ld_stream(k), v0 = ld_stream(v);
+  uint4 k1 = make_uint4(0, 0, 0, 0), v1 = k1;
+  if (kFp8) {
+    k1 = ld_stream(k + 8);
+    v1 = ld_stream(v + 8);
+  }
+  if (slot < 0) return;
+  if (slot >= a.num_slots) {
+    raise_error(a.err, kErrPages);
+    return;
+  }
+  const int64_t to = (slot >> a.page_log2) * a.page_stride +
+                     (slot & ((1 << a.page_log2) - 1)) * a.slot_stride +
+                     h * a.cache_head_stride + c;
+  if (kFp8) {
+    const uint2 ka = cast8(k0, qs_k), kb = cast8(k1, qs_k);
+    const uint2 va = cast8(v0, qs_v), vb = cast8(v1, qs_v);
+    *reinterpret_cast<uint4*>(a.dst[0] + to) = make_uint4(ka.x, ka.y, kb.x, kb.y);
+    *reinterpret_cast<uint4*>(a.dst[1] + to) = make_uint4(va.x, va.y, vb.x, vb.y);
+  } else {
+    *reinterpret_cast<uint4*>(a.dst[0] + 2 * to) = k0;
+    *reinterpret_cast<uint4*>(a.dst[1] + 2 * to) = v0;
   }
 }
 
@@ -513,8 +513,7 @@ cudaError_t launch_kv_write(const KvWriteLaunch& p, cudaStream_t stream) {
   a.qs = p.qs;
   a.err = p.err;
   const int rows_per_cta = kWriteThreads / (p.cache.fp8 ? 8 : 16);
-  int64_t grid = (static_cast<int64_t>(a.rows) + rows_per_cta - 1) / rows_per_cta;
-  if (grid > 148 * 8) grid = 148 * 8;
+  const int64_t grid = (static_cast<int64_t>(a.rows) + rows_per_cta - 1) / rows_per_cta;
   if (p.cache.fp8)
     kv_write_kernel<true><<<static_cast<unsigned>(grid), kWriteThreads, 0, stream>>>(a);
   else
