@@ -560,10 +560,13 @@ kv_tree_keys_kernel(const __grid_constant__ CUtensorMap tm_k,
 // TMEM over the first half of its scores, and feeds the product from there.
 // (The loops over 32 columns stay rolled: a CTA runs a unit's code once or
 // twice, and unrolled it waits for its instructions.)
-// Bound: the chain product, softmax, product of a group (4600 cycles a tile and
-// group, of which the tensor pipe works 2 x 1024 for both groups and the
+// A tile's scores are read once: its maximum, in a pass of its own, only for a
+// row's first reference (before: 8 requests of 4100 and 64 nodes 63.4 us, now
+// 60.8).
+// Bound: the chain product, softmax, product of a group (about 4300 cycles a tile
+// and group, of which the tensor pipe works 2 x 1024 for both groups and the
 // exponentials, 16384 a tile at 16 a cycle, as long): 8 requests x 32768 tokens,
-// 8 KV heads, E4M3: 64 rows 134 us, 128 rows 165 us (830 TFLOP/s); bf16 178 us
+// 8 KV heads, E4M3: 64 rows 132 us, 128 rows 158 us (870 TFLOP/s); bf16 178 us
 // (HBM, 6.0 TB/s) and 188 us.
 // ---------------------------------------------------------------------------
 
@@ -776,7 +779,8 @@ kv_tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
       if (threadIdx.x == 0 && seg.t0 == 0 && seg.t1 < seg.tiles)
         a.join[blockIdx.x] = join_info(seg, items_per_cta(ctl.chunk[C::kThreads], gridDim.x));
       const int ctx = seg.seq - seg.n;
-      const float factor = rows.factor[row];
+      // (not zero: a hidden score is -inf before it is multiplied)
+      const float factor = rows.factor[row] == 0.0f ? 1.17549435e-38f : rows.factor[row];
       const int node = rows.node[row];
       const unsigned long long* mask =
           a.mask + static_cast<int64_t>(seg.q0 + max(node, 0)) * a.mask_words;
@@ -810,12 +814,40 @@ kv_tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
         auto seen = [&](int h) { return h == 0 ? see0 : h == 1 ? see1 : h == 2 ? see2 : see3; };
         w.wait(&ctl.s_full[wg], (g >> 1) & 1);
         tc_fence_after();
-        // ---- the tile's maximum (the scores are read again below: 128 of
-        // them and their exponentials do not fit the registers)
-        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        // ---- a row's first reference: the maximum of its first tile with a
+        // visible key
+        if (__any_sync(0xffffffffu, !set)) {
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+          for (int h = h0; h < h1; ++h) {
+            uint32_t u[32];
+            tmem_ld32(t_s + 32 * h, u);
+            tmem_ld_wait();
+            if (tail) {
+              const uint32_t bits = seen(h);
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!(bits >> c & 1u)) u[c] = 0xFF800000u;
+            }
+#pragma unroll
+            for (int c = 0; c < 32; c += 2)
+              m4[(c / 2) & 3] =
+                  fmax3(m4[(c / 2) & 3], __uint_as_float(u[c]), __uint_as_float(u[c + 1]));
+          }
+          const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * factor;
+          if (!set && m > -INFINITY) {
+            off = kPOffset - m;
+            set = true;
+          }
+        }
+        // ---- P, in one pass: 32 scores become 16 words over scores that were
+        // read already.  A row whose 32 scores exceed its reference by more than
+        // kRefLag moves it by a whole power of two, which rescales the row's
+        // earlier P of this tile, its sum and O without rounding.
+        const uint64_t f2 = f2_pack(factor, factor);
 #pragma unroll 1
         for (int h = h0; h < h1; ++h) {
-          uint32_t u[32];
+          uint32_t u[32], p[16];
           tmem_ld32(t_s + 32 * h, u);
           tmem_ld_wait();
           if (tail) {
@@ -824,54 +856,55 @@ kv_tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
             for (int c = 0; c < 32; ++c)
               if (!(bits >> c & 1u)) u[c] = 0xFF800000u;
           }
+          uint64_t part[2];
+          float m4[4];
+          auto exponentials = [&]() {
+            const uint64_t o2 = f2_pack(off, off);
+            part[0] = part[1] = 0;
 #pragma unroll
-          for (int c = 0; c < 32; c += 2)
-            m4[(c / 2) & 3] = fmax3(m4[(c / 2) & 3], __uint_as_float(u[c]), __uint_as_float(u[c + 1]));
-        }
-        const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * factor;
-        const bool moves = set ? m + off > kPOffset + kRefLag : m > -INFINITY;
-        if (__any_sync(0xffffffffu, moves)) {
-          const float to = moves ? kPOffset - m : off;
-          const float scale = moves && set ? ex2_approx(to - off) : 1.0f;
-          const bool rescale = __any_sync(0xffffffffu, moves && set);
-          off = to;
-          set |= moves;
-          const uint64_t s2 = f2_pack(scale, scale);
-          sum2[0] = f2_mul(sum2[0], s2);
-          sum2[1] = f2_mul(sum2[1], s2);
-          if (rescale) {   // (O is complete: these scores were issued after its last product)
+            for (int c = 0; c < 4; ++c) m4[c] = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+              float x0, x1;
+              f2_unpack(f2_fma(f2_bits(u[c], u[c + 1]), f2, o2), x0, x1);
+              m4[(c / 2) & 3] = fmax3(m4[(c / 2) & 3], x0, x1);
+              const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+              part[(c / 2) & 1] = f2_add(part[(c / 2) & 1], f2_pack(p0, p1));
+              p[c / 2] = kFp8 ? cvt_f16x2(p0, p1) : cvt_bf16x2(p0, p1);
+            }
+          };
+          exponentials();
+          const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          const bool moves = m > kPOffset + kRefLag;
+          if (__any_sync(0xffffffffu, moves)) {
+            const float by = moves ? floorf(kPOffset - m) : 0.0f;
+            const float scale = ex2_approx(by);
+            const uint64_t s2 = f2_pack(scale, scale);
+            off += by;
+            sum2[0] = f2_mul(sum2[0], s2);
+            sum2[1] = f2_mul(sum2[1], s2);
+            tmem_st_wait();
 #pragma unroll 1
-            for (int h = 0; h < 4; ++h) {
-              uint32_t o[32];
-              tmem_ld32(t_o + 32 * h, o);
+            for (int i = h0; i < h; ++i) {
+              tmem_ld16(t_s + 16 * i, p);
               tmem_ld_wait();
 #pragma unroll
-              for (int c = 0; c < 32; ++c)
-                o[c] = __float_as_uint(__uint_as_float(o[c]) * scale);
-              tmem_st32(t_o + 32 * h, o);
+              for (int c = 0; c < 16; ++c) p[c] = kFp8 ? scale_f16x2(p[c], scale) : scale_bf16x2(p[c], scale);
+              tmem_st16(t_s + 16 * i, p);
             }
-          }
-        }
-        // ---- P: 32 scores become 16 words over scores that were read already
-        const uint64_t f2 = f2_pack(factor, factor), o2 = f2_pack(off, off);
+            // (O is complete: these scores were issued after its last product)
 #pragma unroll 1
-        for (int h = h0; h < h1; ++h) {
-          uint32_t u[32], p[16];
-          tmem_ld32(t_s + 32 * h, u);
-          tmem_ld_wait();
-          const uint32_t bits = seen(h);
+            for (int i = 0; i < 8 && g - g0 > 1; ++i) {
+              tmem_ld16(t_o + 16 * i, p);
+              tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            float x0, x1;
-            f2_unpack(f2_fma(f2_bits(u[c], u[c + 1]), f2, o2), x0, x1);
-            if (tail) {
-              if (!(bits >> c & 1u)) x0 = -INFINITY;
-              if (!(bits >> (c + 1) & 1u)) x1 = -INFINITY;
+              for (int c = 0; c < 16; ++c) p[c] = __float_as_uint(__uint_as_float(p[c]) * scale);
+              tmem_st16(t_o + 16 * i, p);
             }
-            const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-            sum2[(c / 2) & 1] = f2_add(sum2[(c / 2) & 1], f2_pack(p0, p1));
-            p[c / 2] = kFp8 ? cvt_f16x2(p0, p1) : cvt_bf16x2(p0, p1);
+            exponentials();
           }
+          sum2[0] = f2_add(sum2[0], part[0]);
+          sum2[1] = f2_add(sum2[1], part[1]);
           tmem_st16(t_s + 16 * h, p);
         }
         if (doubled) {   // the other half's keys

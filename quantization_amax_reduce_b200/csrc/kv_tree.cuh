@@ -117,6 +117,16 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[N]) 
   else tmem_st32(taddr, r);
 }
 
+// A pair times a power of two (exact but for what leaves the type's range).
+__device__ __forceinline__ uint32_t scale_f16x2(uint32_t x, float s) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x));
+  return cvt_f16x2(f.x * s, f.y * s);
+}
+
+__device__ __forceinline__ uint32_t scale_bf16x2(uint32_t x, float s) {
+  return cvt_bf16x2(__uint_as_float(x << 16) * s, __uint_as_float(x & 0xFFFF0000u) * s);
+}
+
 // Reduces N columns (a power of two up to 32) over the warp's lanes: lane l
 // gets column l % N.  N - 1 + log2(32 / N) shuffles instead of 5 N.
 template <int N, bool kMax>

@@ -223,6 +223,27 @@ def test_references_that_move_and_far_tails(nodes, hq, hkv, fp8):
     check(run(s), *expect(s))
 
 
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("nodes,hq,hkv", [(2, 8, 1), (7, 4, 1), (13, 4, 1), (30, 4, 1), (40, 4, 1)])
+def test_references_that_move_inside_a_tile(nodes, hq, hkv, fp8):
+    """Scores that climb (for every other query: fall) by 2^9 and 2^18 every 32
+    keys, within each tile and a little higher in each, over several tiles."""
+    L, page = 900, 16
+    s = make(40 + nodes, [L], [nodes], hq, hkv, page, fp8)
+    unit = np.sign(s["q"][0, 0].double().numpy())
+    rows = np.arange(nodes * hq).reshape(nodes, hq)
+    size = np.where(rows % 2, -4.0, 4.0) / (1 + rows // 2 % 2)
+    s["q"] = torch.from_numpy(size[..., None] * unit).to(torch.bfloat16)
+    for p in range(L):
+        level = (0.02 + 0.14 * (p // 16 % 8)) * (0.3 + 0.7 * p / L)
+        s["values"][0][s["tables"][0][p // page], p % page] = unit * level * (64 if fp8 else 1)
+    c = torch.from_numpy(s["values"][0])
+    c = c.to(torch.float8_e4m3fn) if fp8 else c.to(torch.bfloat16)
+    s["values"][0][:] = c.double().numpy()
+    s["caches"][0] = (c.view(torch.uint8) if fp8 else c).to(DEV)
+    check(run(s), *expect(s))
+
+
 @pytest.mark.parametrize("nodes,hq,hkv", [(6, 2, 1), (6, 4, 1), (12, 4, 1), (40, 4, 1)])
 def test_query_rows_of_very_different_sizes(nodes, hq, hkv):
     """E4M3: rows that cannot share a scale, rows of zeros, one with an infinity."""
