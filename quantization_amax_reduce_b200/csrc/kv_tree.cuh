@@ -385,16 +385,17 @@ __device__ __forceinline__ void produce(const TreeArgs& a, const Waits& w, const
   int g = 0, stage = 0, turn = 0;
   while (!w.aborted() && walk.next(a, chunk, seg)) {
     const int32_t* table = a.tables + seg.b * a.table_stride;
+    // this lane's first key of a tile; it has a page to load if the key is one
+    auto first_key = [&](int t) { return t * kTile + (w.lane << box_log2); };
+    auto has_page = [&](int t) { return w.lane < kTile >> box_log2 && first_key(t) < seg.seq; };
     auto look_up = [&](int t) {
-      const int key = t * kTile + (w.lane << box_log2);
-      if (w.lane >= kTile >> box_log2 || key >= seg.seq) return -2;
-      return __ldg(table + (key >> a.page_log2));
+      return has_page(t) ? __ldg(table + (first_key(t) >> a.page_log2)) : 0;
     };
     int next_id = look_up(seg.t0);
     for (int t = seg.t0; t < seg.t1; ++t, ++g) {
       const int id = next_id;
       if (t + 1 < seg.t1) next_id = look_up(t + 1);
-      const bool load = id != -2;
+      const bool load = has_page(t);   // (whatever its id: no id means "none")
       if (report && load && (id < 0 || id >= a.num_pages)) raise_error(a.err, kErrPages);
       const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, load)) * box * (kFp8 ? 128 : 256);
       const int row = a.page_log2 > 7 ? (t * kTile) & (page - 1) : 0;

@@ -490,3 +490,25 @@ def test_empty_calls():
     qar.kv_tree_fwd(a[0][:1], a[1], a[2], a[3], zero[:1], zero, 0, 0, out=out, error=err)
     torch.cuda.synchronize()
     assert (out == 3).all() and qar.read_error_word(err) == 0
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("nodes", [1, 7, 20])       # 16 and 32 columns, rows on the lanes
+@pytest.mark.parametrize("bad", [-2, -1, -(2 ** 31), "end", 2 ** 31 - 1])
+def test_any_page_id_outside_the_cache_reads_as_zeros(bad, nodes, fp8):
+    """Whatever the id is, its page's keys and values are zeros, not what an
+    earlier tile left in shared memory, and the call reports it."""
+    s = make(41, [300, 150, 300], [nodes] * 3, 4, 1, 16, fp8)
+    run(s)                                            # (shared memory is full of rows now)
+    zero = len(s["values"][0])
+    args = to_dev(s)
+    tables = args[3].clone()
+    for b, page in ((0, 12), (1, 0), (2, 18)):        # the last: the page of the nodes
+        tables[b, page] = zero if bad == "end" else bad
+        s["tables"][b, page] = zero
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = qar.kv_tree_fwd(*args[:3], tables, *args[4:], error=err)
+    torch.cuda.synchronize()
+    assert qar.read_error_word(err) == 7
+    s["values"] = [np.concatenate([v, np.zeros_like(v[:1])]) for v in s["values"]]
+    check(out, *expect(s))
