@@ -518,7 +518,8 @@ int fp8attn_quantize_qkv_noalloc_error(void* stream);
 
 /* Device pointers to a layer's static {qs_q, qs_k, qs_v} and {ds_q, ds_k,
  * ds_v}: a cache outlives the layer's current scales, so its scales are the
- * static ones.  NULL on a bad argument or without static bounds. */
+ * static ones.  NULL on a bad argument or without static bounds (the calls
+ * below refuse a NULL that is passed on). */
 const float* fp8attn_static_quant_scale_ptr(fp8attn_ctx* ctx, int layer);
 const float* fp8attn_static_descale_ptr(fp8attn_ctx* ctx, int layer);
 
@@ -556,15 +557,15 @@ fp8attn_status fp8attn_kv_assign_pages(const int32_t* d_seq_lens, const int32_t*
                                        int64_t max_tokens, int32_t* d_cu_new, int64_t* d_slots,
                                        int32_t* d_positions, int32_t* d_error, void* stream);
 
-/* Write the K and V of new tokens into their slots.  k, v: bf16 sources as in
- * fp8attn_quantize_qkv, one row per entry of d_slots (int64[tokens]).
- * d_quant_scale_qkv: device {qs_q, qs_k, qs_v}; the cache then holds E4M3
- * codes e4m3(fl32(x * qs)), as the quantisation kernels cast.  NULL: a bf16
- * cache, x unchanged.  A negative slot is skipped; one beyond the cache is
- * skipped and sets PAGES.  Slots must be distinct: of two tokens with one
- * slot either's 16-byte pieces may remain.  Errors: INVALID, UNSUPPORTED
+/* Write the K and V of new tokens into their slots of an E4M3 cache.  k, v:
+ * bf16 sources as in fp8attn_quantize_qkv, one row per entry of d_slots
+ * (int64[tokens]).  d_quant_scale_qkv: device {qs_q, qs_k, qs_v}; the cache
+ * receives the codes e4m3(fl32(x * qs)), as the quantisation kernels cast.  A
+ * negative slot is skipped; one beyond the cache is skipped and sets PAGES.
+ * Slots must be distinct: of two tokens with one slot either's 16-byte pieces
+ * may remain.  Errors: INVALID (a NULL scale among them), UNSUPPORTED
  * (head_dim != 128, page_size, strides or alignment, tokens * heads >= 2^31),
- * CUDA.  tokens == 0 launches nothing. */
+ * CUDA.  tokens == 0 launches nothing (and needs no scale). */
 fp8attn_status fp8attn_kv_write(const void* k, const void* v, int64_t tok_stride,
                                 int64_t head_stride, const int64_t* d_slots, int64_t tokens,
                                 int num_kv_heads, int head_dim, void* k_cache, void* v_cache,
@@ -572,13 +573,21 @@ fp8attn_status fp8attn_kv_write(const void* k, const void* v, int64_t tok_stride
                                 int64_t cache_head_stride, int num_pages, int page_size,
                                 const float* d_quant_scale_qkv, int32_t* d_error, void* stream);
 
-/* Bytes of device workspace fp8attn_kv_tree_fwd needs for these bounds (0 if
- * it needs none, or on a bad argument). */
+/* The same for a bf16 cache: x unchanged, no scale. */
+fp8attn_status fp8attn_kv_write_bf16(const void* k, const void* v, int64_t tok_stride,
+                                     int64_t head_stride, const int64_t* d_slots, int64_t tokens,
+                                     int num_kv_heads, int head_dim, void* k_cache, void* v_cache,
+                                     int64_t page_stride, int64_t slot_stride,
+                                     int64_t cache_head_stride, int num_pages, int page_size,
+                                     int32_t* d_error, void* stream);
+
+/* Bytes of device workspace fp8attn_kv_tree_fwd and fp8attn_kv_tree_fwd_bf16
+ * need for these bounds (0 if they need none, or on a bad argument). */
 size_t fp8attn_kv_tree_workspace_bytes(int rows, int max_q_len, int max_seqlen, int num_heads,
                                        int num_kv_heads);
 
-/* Attention of new tokens over the cache: a drafted tree, a chain, or a single
- * token per request.  Request b's n_b = cu_q[b+1] - cu_q[b] queries (rows
+/* Attention of new tokens over an E4M3 cache: a drafted tree, a chain, or a
+ * single token per request.  Request b's n_b = cu_q[b+1] - cu_q[b] queries (rows
  * cu_q[b].. of q, bf16 [total_q, num_heads, 128] with element strides, 16-byte
  * aligned) are the last n_b of its d_seq_lens[b] positions, whose K and V are
  * in the cache already.  Query i sees every position before those, and node m
@@ -591,8 +600,8 @@ size_t fp8attn_kv_tree_workspace_bytes(int rows, int max_q_len, int max_seqlen, 
  * table_width).
  *   out[i] = ds_v sum_j p_j v_j / sum_j p_j,
  *   p_j = exp(softmax_scale ds_k q_i . k_j - max)
- * d_descale_qkv: device {ds_q, ds_k, ds_v} for an E4M3 cache (q is bf16, ds_q
- * unused); NULL for a bf16 cache.  softmax_scale 0 selects 1/sqrt(head_dim).
+ * d_descale_qkv: device {ds_q, ds_k, ds_v} (q is bf16, ds_q unused).
+ * softmax_scale 0 selects 1/sqrt(head_dim).
  * max_q_len, max_seqlen: bounds of n_b and of the lengths.  out: bf16 packed
  * [total_q, num_heads, 128]; rows of no request stay as they are.  workspace:
  * fp8attn_kv_tree_workspace_bytes of device memory (16-byte aligned), used by
@@ -603,8 +612,8 @@ size_t fp8attn_kv_tree_workspace_bytes(int rows, int max_q_len, int max_seqlen, 
  * total_q, or more than 64 mask_words nodes: it is left out, its rows stay as
  * they are), PAGES (a page id outside the cache: its keys and values are read
  * as zeros), TIMEOUT (out is then undefined).
- * Errors: INVALID (null pointers, negative sizes, num_heads not a multiple of
- * num_kv_heads, a workspace too small, a bad softmax_scale), UNSUPPORTED
+ * Errors: INVALID (null pointers, the descale's too, negative sizes, num_heads
+ * not a multiple of num_kv_heads, a workspace too small, a bad softmax_scale), UNSUPPORTED
  * (head_dim != 128, page_size, strides or alignment, rows > 2048, total_q *
  * num_heads >= 2^31, num_heads / num_kv_heads = G > 1024, max_q_len * G * G
  * close to 2^32, max_seqlen > 2^31 - 256, bounds that allow 2^31 or more
@@ -623,6 +632,20 @@ fp8attn_status fp8attn_kv_tree_fwd(const void* q, int64_t q_tok_stride, int64_t 
                                    const int64_t* d_tree_mask, int mask_words,
                                    float softmax_scale, void* out, void* workspace,
                                    size_t workspace_bytes, int32_t* d_error, void* stream);
+
+/* The same over a bf16 cache: ds_k = ds_v = 1. */
+fp8attn_status fp8attn_kv_tree_fwd_bf16(const void* q, int64_t q_tok_stride, int64_t q_head_stride,
+                                        const void* k_cache, const void* v_cache,
+                                        int64_t page_stride, int64_t slot_stride,
+                                        int64_t cache_head_stride, int num_pages, int page_size,
+                                        const int32_t* d_block_tables, int64_t table_stride,
+                                        int table_width, const int32_t* d_seq_lens,
+                                        const int32_t* d_cu_q, int rows, int max_q_len,
+                                        int max_seqlen, int64_t total_q, int num_heads,
+                                        int num_kv_heads, int head_dim,
+                                        const int64_t* d_tree_mask, int mask_words,
+                                        float softmax_scale, void* out, void* workspace,
+                                        size_t workspace_bytes, int32_t* d_error, void* stream);
 
 /* After verification: request b keeps d_keep_lens[b] of its n_b drafted
  * nodes, d_paths[b][0] < d_paths[b][1] < ... (int32 [rows, depth], row stride

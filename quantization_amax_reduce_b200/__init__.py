@@ -118,9 +118,14 @@ def lib() -> ctypes.CDLL:
         "fp8attn_kv_assign_pages": (I, [P, P, I, I, P, I64, I, P, P, I, P, I64, P, P, P, P, P]),
         "fp8attn_kv_write": (I, [P, P, I64, I64, P, I64, I, I, P, P, I64, I64, I64, I, I, P, P,
                                  P]),
+        "fp8attn_kv_write_bf16": (I, [P, P, I64, I64, P, I64, I, I, P, P, I64, I64, I64, I, I, P,
+                                      P]),
         "fp8attn_kv_tree_workspace_bytes": (ctypes.c_size_t, [I, I, I, I, I]),
         "fp8attn_kv_tree_fwd": (I, [P, I64, I64, P, P, I64, I64, I64, I, I, P, I64, I, P, P, I, I,
                                     I, I64, I, I, I, P, P, I, F, P, P, ctypes.c_size_t, P, P]),
+        "fp8attn_kv_tree_fwd_bf16": (I, [P, I64, I64, P, P, I64, I64, I64, I, I, P, I64, I, P, P,
+                                         I, I, I, I64, I, I, I, P, I, F, P, P, ctypes.c_size_t, P,
+                                         P]),
         "fp8attn_kv_keep_path": (I, [P, P, I64, I64, I64, I, I, I, I, I, P, I64, I, P, P, I, P,
                                      I64, I, P, P, P]),
         "fp8attn_apply_margin": (I, [P, I64, F, P]),
@@ -604,8 +609,8 @@ def _native():
         except ImportError as e:
             raise RuntimeError("the _calls module is missing: build it with "
                                "`python -m quantization_amax_reduce_b200.build`") from e
-        entries = (L.fp8attn_kv_assign_pages, L.fp8attn_kv_write, L.fp8attn_kv_tree_fwd,
-                   L.fp8attn_kv_keep_path)
+        entries = (L.fp8attn_kv_assign_pages, L.fp8attn_kv_write, L.fp8attn_kv_write_bf16,
+                   L.fp8attn_kv_tree_fwd, L.fp8attn_kv_tree_fwd_bf16, L.fp8attn_kv_keep_path)
         module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in entries), torch.Tensor, _I32)
         _native_calls = module
     return _native_calls
@@ -655,6 +660,8 @@ def _scale3(scale, name: str, fp8: bool, device) -> int:
                 scale.device != device:
             raise ValueError(f"{name} must be 3 contiguous fp32 values on {device}")
         return scale.data_ptr()
+    if not int(scale):   # (what a getter of the C ABI gives for a layer without static scales)
+        raise ValueError(f"{name} is a null pointer")
     return int(scale)
 
 
@@ -747,7 +754,7 @@ def kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: tor
     head_stride = steps[1] if heads > 1 else HEAD_DIM
     handle, on = _launch_on(stream, dev)
     with on:
-        status = C.write(
+        status = (C.write if fp8 else C.write_bf16)(
             k.data_ptr(), v.data_ptr(), tok_stride, head_stride, slots.data_ptr(), T, heads,
             HEAD_DIM, k_cache.data_ptr(), v_cache.data_ptr(), strides[0], strides[1], strides[2],
             pages, page_size, scale, err, handle)
@@ -807,7 +814,7 @@ def kv_tree_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
         else:
             _check_out(out, "out", _BF16, T * heads * HEAD_DIM, dev)
         work = seq_lens.new_empty(need) if need else None
-        status = C.tree_fwd(
+        status = (C.tree_fwd if fp8 else C.tree_fwd_bf16)(
             q.data_ptr(), tok_stride, head_stride, k_cache.data_ptr(), v_cache.data_ptr(),
             strides[0], strides[1], strides[2], pages, page_size, tables, table_stride, width,
             seq, cu, rows, max_q_len, max_seqlen, T, heads, kv_heads, HEAD_DIM, scale, mask,

@@ -140,6 +140,109 @@ fp8attn_status check_cache(const void* k, const void* v, int64_t page_stride, in
   return FP8ATTN_OK;
 }
 
+// (`fp8` says what the cache holds; a scale does not, since a missing one must
+// not turn an E4M3 cache into a bf16 one of twice the bytes)
+fp8attn_status run_kv_write(const void* k, const void* v, int64_t tok_stride, int64_t head_stride,
+                            const int64_t* d_slots, int64_t tokens, int num_kv_heads, int head_dim,
+                            void* k_cache, void* v_cache, int64_t page_stride, int64_t slot_stride,
+                            int64_t cache_head_stride, int num_pages, int page_size, bool fp8,
+                            const float* qs, int32_t* d_error, void* stream) {
+  if (tokens < 0) return FP8ATTN_ERR_INVALID;
+  KvWriteLaunch p;
+  const fp8attn_status st =
+      check_cache(k_cache, v_cache, page_stride, slot_stride, cache_head_stride, num_pages,
+                  page_size, num_kv_heads, head_dim, fp8, &p.cache);
+  if (st != FP8ATTN_OK || tokens == 0) return st;
+  if (!k || !v || !d_slots) return FP8ATTN_ERR_INVALID;
+  if (tok_stride <= 0 || head_stride <= 0 || (tok_stride % 8) || (head_stride % 8) ||
+      !aligned(k, 16) || !aligned(v, 16) || !aligned(d_slots, 8) ||
+      tokens > 0x7FFFFFFFLL / num_kv_heads)
+    return FP8ATTN_ERR_UNSUPPORTED;
+  p.k = k;
+  p.v = v;
+  p.tok_stride = tok_stride;
+  p.head_stride = head_stride;
+  p.slots = d_slots;
+  p.tokens = tokens;
+  p.qs = qs;
+  p.err = d_error;
+  if (launch_kv_write(p, as_stream(stream)) != cudaSuccess) return FP8ATTN_ERR_CUDA;
+  g_launches.fetch_add(1);
+  return FP8ATTN_OK;
+}
+
+fp8attn_status run_kv_tree(const void* q, int64_t q_tok_stride, int64_t q_head_stride,
+                           const void* k_cache, const void* v_cache, int64_t page_stride,
+                           int64_t slot_stride, int64_t cache_head_stride, int num_pages,
+                           int page_size, const int32_t* d_block_tables, int64_t table_stride,
+                           int table_width, const int32_t* d_seq_lens, const int32_t* d_cu_q,
+                           int rows, int max_q_len, int max_seqlen, int64_t total_q, int num_heads,
+                           int num_kv_heads, int head_dim, bool fp8, const float* descale,
+                           const int64_t* d_tree_mask, int mask_words, float softmax_scale,
+                           void* out, void* workspace, size_t workspace_bytes, int32_t* d_error,
+                           void* stream) {
+  if (rows < 0 || max_q_len < 0 || max_seqlen < 0 || total_q < 0 || num_heads < 1 ||
+      num_kv_heads < 1 || num_heads % num_kv_heads || table_width < 1 ||
+      (d_tree_mask && mask_words < 1))
+    return FP8ATTN_ERR_INVALID;
+  if (!(softmax_scale >= 0.0f) || std::isinf(softmax_scale)) return FP8ATTN_ERR_INVALID;
+  KvTreeLaunch p;
+  const fp8attn_status st =
+      check_cache(k_cache, v_cache, page_stride, slot_stride, cache_head_stride, num_pages,
+                  page_size, num_kv_heads, head_dim, fp8, &p.cache);
+  if (st != FP8ATTN_OK) return st;
+  if (rows > kMaxTreeRows) return FP8ATTN_ERR_UNSUPPORTED;
+  if (rows == 0 || total_q == 0) return FP8ATTN_OK;
+  if (rows > 1 && table_stride < table_width) return FP8ATTN_ERR_INVALID;
+  if (!q || !out || !d_block_tables || !d_seq_lens || !d_cu_q) return FP8ATTN_ERR_INVALID;
+  if (q_tok_stride <= 0 || q_head_stride <= 0 || (q_tok_stride % 8) || (q_head_stride % 8) ||
+      !aligned(q, 16) || !aligned(out, 16) || !aligned(d_tree_mask, 8) ||
+      total_q > 0x7FFFFFFFLL / num_heads ||
+      (num_heads / num_kv_heads) > 1024)
+    return FP8ATTN_ERR_UNSUPPORTED;
+  // no request has more queries than there are, nor tokens than its table holds
+  if (max_q_len > total_q) max_q_len = static_cast<int>(total_q);
+  const int64_t held = static_cast<int64_t>(table_width) * page_size;
+  if (max_seqlen > held) max_seqlen = static_cast<int>(held);
+  // the kernels hold query rows, positions and their ends (a tile further) in
+  // 32 bits, and divide query rows by the group in 32 bits
+  const int64_t group = num_heads / num_kv_heads;
+  if ((max_q_len * group + 128) * group > 0xFFFFFFFFLL || max_q_len * group > 0x7FFFFF00LL ||
+      max_seqlen > 0x7FFFFF00LL ||
+      kv_tree_max_items(rows, max_q_len, max_seqlen, num_heads, num_kv_heads) > 0x7FFFFFFFLL)
+    return FP8ATTN_ERR_UNSUPPORTED;
+  const size_t need =
+      max_q_len && max_seqlen
+          ? kv_tree_workspace_bytes(rows, max_q_len, max_seqlen, num_heads, num_kv_heads)
+          : 0;
+  if (need > workspace_bytes || (need && !workspace)) return FP8ATTN_ERR_INVALID;
+  if (!aligned(workspace, 16)) return FP8ATTN_ERR_UNSUPPORTED;
+  p.q = q;
+  p.q_tok_stride = q_tok_stride;
+  p.q_head_stride = q_head_stride;
+  p.tables = d_block_tables;
+  p.table_stride = table_stride;
+  p.width = table_width;
+  p.seq = d_seq_lens;
+  p.cu = d_cu_q;
+  p.rows = rows;
+  p.max_q = max_q_len;
+  p.max_seqlen = max_seqlen;
+  p.total_q = total_q;
+  p.heads = num_heads;
+  p.descale = descale;
+  p.mask = d_tree_mask;
+  p.mask_words = mask_words;
+  p.softmax_scale = softmax_scale == 0.0f ? 1.0f / std::sqrt(static_cast<float>(head_dim))
+                                          : softmax_scale;
+  p.out = out;
+  p.workspace = workspace;
+  p.err = d_error;
+  if (launch_kv_tree(p, as_stream(stream)) != cudaSuccess) return FP8ATTN_ERR_CUDA;
+  g_launches.fetch_add(1);
+  return FP8ATTN_OK;
+}
+
 }  // namespace
 
 void fp8attn::note_launch() { g_launches.fetch_add(1); }
@@ -735,28 +838,21 @@ fp8attn_status fp8attn_kv_write(const void* k, const void* v, int64_t tok_stride
                                 int64_t page_stride, int64_t slot_stride,
                                 int64_t cache_head_stride, int num_pages, int page_size,
                                 const float* d_quant_scale_qkv, int32_t* d_error, void* stream) {
-  if (tokens < 0) return FP8ATTN_ERR_INVALID;
-  KvWriteLaunch p;
-  const fp8attn_status st =
-      check_cache(k_cache, v_cache, page_stride, slot_stride, cache_head_stride, num_pages,
-                  page_size, num_kv_heads, head_dim, d_quant_scale_qkv != nullptr, &p.cache);
-  if (st != FP8ATTN_OK || tokens == 0) return st;
-  if (!k || !v || !d_slots) return FP8ATTN_ERR_INVALID;
-  if (tok_stride <= 0 || head_stride <= 0 || (tok_stride % 8) || (head_stride % 8) ||
-      !aligned(k, 16) || !aligned(v, 16) || !aligned(d_slots, 8) ||
-      tokens > 0x7FFFFFFFLL / num_kv_heads)
-    return FP8ATTN_ERR_UNSUPPORTED;
-  p.k = k;
-  p.v = v;
-  p.tok_stride = tok_stride;
-  p.head_stride = head_stride;
-  p.slots = d_slots;
-  p.tokens = tokens;
-  p.qs = d_quant_scale_qkv;
-  p.err = d_error;
-  if (launch_kv_write(p, as_stream(stream)) != cudaSuccess) return FP8ATTN_ERR_CUDA;
-  g_launches.fetch_add(1);
-  return FP8ATTN_OK;
+  if (!d_quant_scale_qkv && tokens > 0) return FP8ATTN_ERR_INVALID;
+  return run_kv_write(k, v, tok_stride, head_stride, d_slots, tokens, num_kv_heads, head_dim,
+                      k_cache, v_cache, page_stride, slot_stride, cache_head_stride, num_pages,
+                      page_size, d_quant_scale_qkv != nullptr, d_quant_scale_qkv, d_error, stream);
+}
+
+fp8attn_status fp8attn_kv_write_bf16(const void* k, const void* v, int64_t tok_stride,
+                                     int64_t head_stride, const int64_t* d_slots, int64_t tokens,
+                                     int num_kv_heads, int head_dim, void* k_cache, void* v_cache,
+                                     int64_t page_stride, int64_t slot_stride,
+                                     int64_t cache_head_stride, int num_pages, int page_size,
+                                     int32_t* d_error, void* stream) {
+  return run_kv_write(k, v, tok_stride, head_stride, d_slots, tokens, num_kv_heads, head_dim,
+                      k_cache, v_cache, page_stride, slot_stride, cache_head_stride, num_pages,
+                      page_size, false, nullptr, d_error, stream);
 }
 
 size_t fp8attn_kv_tree_workspace_bytes(int rows, int max_q_len, int max_seqlen, int num_heads,
@@ -779,66 +875,31 @@ fp8attn_status fp8attn_kv_tree_fwd(const void* q, int64_t q_tok_stride, int64_t 
                                    const int64_t* d_tree_mask, int mask_words,
                                    float softmax_scale, void* out, void* workspace,
                                    size_t workspace_bytes, int32_t* d_error, void* stream) {
-  if (rows < 0 || max_q_len < 0 || max_seqlen < 0 || total_q < 0 || num_heads < 1 ||
-      num_kv_heads < 1 || num_heads % num_kv_heads || table_width < 1 ||
-      (d_tree_mask && mask_words < 1))
-    return FP8ATTN_ERR_INVALID;
-  if (!(softmax_scale >= 0.0f) || std::isinf(softmax_scale)) return FP8ATTN_ERR_INVALID;
-  KvTreeLaunch p;
-  const fp8attn_status st =
-      check_cache(k_cache, v_cache, page_stride, slot_stride, cache_head_stride, num_pages,
-                  page_size, num_kv_heads, head_dim, d_descale_qkv != nullptr, &p.cache);
-  if (st != FP8ATTN_OK) return st;
-  if (rows > kMaxTreeRows) return FP8ATTN_ERR_UNSUPPORTED;
-  if (rows == 0 || total_q == 0) return FP8ATTN_OK;
-  if (rows > 1 && table_stride < table_width) return FP8ATTN_ERR_INVALID;
-  if (!q || !out || !d_block_tables || !d_seq_lens || !d_cu_q) return FP8ATTN_ERR_INVALID;
-  if (q_tok_stride <= 0 || q_head_stride <= 0 || (q_tok_stride % 8) || (q_head_stride % 8) ||
-      !aligned(q, 16) || !aligned(out, 16) || !aligned(d_tree_mask, 8) ||
-      total_q > 0x7FFFFFFFLL / num_heads ||
-      (num_heads / num_kv_heads) > 1024)
-    return FP8ATTN_ERR_UNSUPPORTED;
-  // no request has more queries than there are, nor tokens than its table holds
-  if (max_q_len > total_q) max_q_len = static_cast<int>(total_q);
-  const int64_t held = static_cast<int64_t>(table_width) * page_size;
-  if (max_seqlen > held) max_seqlen = static_cast<int>(held);
-  // the kernels hold query rows, positions and their ends (a tile further) in
-  // 32 bits, and divide query rows by the group in 32 bits
-  const int64_t group = num_heads / num_kv_heads;
-  if ((max_q_len * group + 128) * group > 0xFFFFFFFFLL || max_q_len * group > 0x7FFFFF00LL ||
-      max_seqlen > 0x7FFFFF00LL ||
-      kv_tree_max_items(rows, max_q_len, max_seqlen, num_heads, num_kv_heads) > 0x7FFFFFFFLL)
-    return FP8ATTN_ERR_UNSUPPORTED;
-  const size_t need =
-      max_q_len && max_seqlen
-          ? kv_tree_workspace_bytes(rows, max_q_len, max_seqlen, num_heads, num_kv_heads)
-          : 0;
-  if (need > workspace_bytes || (need && !workspace)) return FP8ATTN_ERR_INVALID;
-  if (!aligned(workspace, 16)) return FP8ATTN_ERR_UNSUPPORTED;
-  p.q = q;
-  p.q_tok_stride = q_tok_stride;
-  p.q_head_stride = q_head_stride;
-  p.tables = d_block_tables;
-  p.table_stride = table_stride;
-  p.width = table_width;
-  p.seq = d_seq_lens;
-  p.cu = d_cu_q;
-  p.rows = rows;
-  p.max_q = max_q_len;
-  p.max_seqlen = max_seqlen;
-  p.total_q = total_q;
-  p.heads = num_heads;
-  p.descale = d_descale_qkv;
-  p.mask = d_tree_mask;
-  p.mask_words = mask_words;
-  p.softmax_scale = softmax_scale == 0.0f ? 1.0f / std::sqrt(static_cast<float>(head_dim))
-                                          : softmax_scale;
-  p.out = out;
-  p.workspace = workspace;
-  p.err = d_error;
-  if (launch_kv_tree(p, as_stream(stream)) != cudaSuccess) return FP8ATTN_ERR_CUDA;
-  g_launches.fetch_add(1);
-  return FP8ATTN_OK;
+  if (!d_descale_qkv) return FP8ATTN_ERR_INVALID;
+  return run_kv_tree(q, q_tok_stride, q_head_stride, k_cache, v_cache, page_stride, slot_stride,
+                     cache_head_stride, num_pages, page_size, d_block_tables, table_stride,
+                     table_width, d_seq_lens, d_cu_q, rows, max_q_len, max_seqlen, total_q,
+                     num_heads, num_kv_heads, head_dim, true, d_descale_qkv, d_tree_mask,
+                     mask_words, softmax_scale, out, workspace, workspace_bytes, d_error, stream);
+}
+
+fp8attn_status fp8attn_kv_tree_fwd_bf16(const void* q, int64_t q_tok_stride, int64_t q_head_stride,
+                                        const void* k_cache, const void* v_cache,
+                                        int64_t page_stride, int64_t slot_stride,
+                                        int64_t cache_head_stride, int num_pages, int page_size,
+                                        const int32_t* d_block_tables, int64_t table_stride,
+                                        int table_width, const int32_t* d_seq_lens,
+                                        const int32_t* d_cu_q, int rows, int max_q_len,
+                                        int max_seqlen, int64_t total_q, int num_heads,
+                                        int num_kv_heads, int head_dim,
+                                        const int64_t* d_tree_mask, int mask_words,
+                                        float softmax_scale, void* out, void* workspace,
+                                        size_t workspace_bytes, int32_t* d_error, void* stream) {
+  return run_kv_tree(q, q_tok_stride, q_head_stride, k_cache, v_cache, page_stride, slot_stride,
+                     cache_head_stride, num_pages, page_size, d_block_tables, table_stride,
+                     table_width, d_seq_lens, d_cu_q, rows, max_q_len, max_seqlen, total_q,
+                     num_heads, num_kv_heads, head_dim, false, nullptr, d_tree_mask,
+                     mask_words, softmax_scale, out, workspace, workspace_bytes, d_error, stream);
 }
 
 fp8attn_status fp8attn_kv_keep_path(void* k_cache, void* v_cache, int64_t page_stride,

@@ -15,7 +15,9 @@
 
 static __typeof__(&fp8attn_kv_assign_pages) p_assign;
 static __typeof__(&fp8attn_kv_write) p_write;
+static __typeof__(&fp8attn_kv_write_bf16) p_write_bf16;
 static __typeof__(&fp8attn_kv_tree_fwd) p_tree;
+static __typeof__(&fp8attn_kv_tree_fwd_bf16) p_tree_bf16;
 static __typeof__(&fp8attn_kv_keep_path) p_keep;
 static PyObject *tensor_type, *int32_dtype;
 static PyObject *s_dtype, *s_get_device, *s_is_contiguous, *s_numel, *s_data_ptr;
@@ -73,6 +75,25 @@ static PyObject* write_kv(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   return PyLong_FromLong(st);
 }
 
+/* A scale's place in the arguments of the bf16 calls, which take the same
+ * ones: it must be 0. */
+static int no_scale(int64_t scale) {
+  if (scale) PyErr_SetString(PyExc_ValueError, "a bf16 cache takes no scale");
+  return !scale;
+}
+
+static PyObject* write_bf16(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  int64_t v[18];
+  int st;
+  (void)self;
+  if (!take(a, n, "ppllpliipplll" "iippp", v, NULL) || !no_scale(v[15])) return NULL;
+  Py_BEGIN_ALLOW_THREADS
+  st = p_write_bf16(PTR(0), PTR(1), v[2], v[3], PTR(4), v[5], I32(6), I32(7), PTR(8), PTR(9),
+                    v[10], v[11], v[12], I32(13), I32(14), PTR(16), PTR(17));
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(st);
+}
+
 static PyObject* tree_fwd(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   int64_t v[31];
   float scale = 0.0f;
@@ -84,6 +105,23 @@ static PyObject* tree_fwd(PyObject* self, PyObject* const* a, Py_ssize_t n) {
               v[11], I32(12), PTR(13), PTR(14), I32(15), I32(16), I32(17), v[18], I32(19),
               I32(20), I32(21), PTR(22), PTR(23), I32(24), scale, PTR(26), PTR(27),
               (size_t)v[28], PTR(29), PTR(30));
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(st);
+}
+
+static PyObject* tree_fwd_bf16(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  int64_t v[31];
+  float scale = 0.0f;
+  int st;
+  (void)self;
+  if (!take(a, n, "pllpplll" "ii" "pli" "pp" "iii" "liii" "ppi" "f" "pplpp", v, &scale) ||
+      !no_scale(v[22]))
+    return NULL;
+  Py_BEGIN_ALLOW_THREADS
+  st = p_tree_bf16(PTR(0), v[1], v[2], PTR(3), PTR(4), v[5], v[6], v[7], I32(8), I32(9), PTR(10),
+                   v[11], I32(12), PTR(13), PTR(14), I32(15), I32(16), I32(17), v[18], I32(19),
+                   I32(20), I32(21), PTR(23), I32(24), scale, PTR(26), PTR(27), (size_t)v[28],
+                   PTR(29), PTR(30));
   Py_END_ALLOW_THREADS
   return PyLong_FromLong(st);
 }
@@ -151,30 +189,35 @@ static PyObject* int32_ptr(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   return PyObject_CallMethodNoArgs(t, s_data_ptr);
 }
 
-/* bind(assign_pages, write, tree_fwd, keep_path, torch.Tensor, torch.int32) */
+/* bind(assign_pages, write, write_bf16, tree_fwd, tree_fwd_bf16, keep_path,
+ *      torch.Tensor, torch.int32) */
 static PyObject* bind(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  int64_t v[4];
+  int64_t v[6];
   (void)self;
-  if (n != 6 || !PyType_Check(a[4])) {
-    PyErr_SetString(PyExc_TypeError, "bind(four addresses, tensor type, int32)");
+  if (n != 8 || !PyType_Check(a[6])) {
+    PyErr_SetString(PyExc_TypeError, "bind(six addresses, tensor type, int32)");
     return NULL;
   }
-  if (!take(a, 4, "pppp", v, NULL)) return NULL;
+  if (!take(a, 6, "pppppp", v, NULL)) return NULL;
   p_assign = (__typeof__(p_assign))(intptr_t)v[0];
   p_write = (__typeof__(p_write))(intptr_t)v[1];
-  p_tree = (__typeof__(p_tree))(intptr_t)v[2];
-  p_keep = (__typeof__(p_keep))(intptr_t)v[3];
-  Py_INCREF(a[4]);
-  Py_XSETREF(tensor_type, a[4]);
-  Py_INCREF(a[5]);
-  Py_XSETREF(int32_dtype, a[5]);
+  p_write_bf16 = (__typeof__(p_write_bf16))(intptr_t)v[2];
+  p_tree = (__typeof__(p_tree))(intptr_t)v[3];
+  p_tree_bf16 = (__typeof__(p_tree_bf16))(intptr_t)v[4];
+  p_keep = (__typeof__(p_keep))(intptr_t)v[5];
+  Py_INCREF(a[6]);
+  Py_XSETREF(tensor_type, a[6]);
+  Py_INCREF(a[7]);
+  Py_XSETREF(int32_dtype, a[7]);
   Py_RETURN_NONE;
 }
 
 static PyMethodDef methods[] = {
     {"assign_pages", (PyCFunction)(void (*)(void))assign_pages, METH_FASTCALL, NULL},
     {"write", (PyCFunction)(void (*)(void))write_kv, METH_FASTCALL, NULL},
+    {"write_bf16", (PyCFunction)(void (*)(void))write_bf16, METH_FASTCALL, NULL},
     {"tree_fwd", (PyCFunction)(void (*)(void))tree_fwd, METH_FASTCALL, NULL},
+    {"tree_fwd_bf16", (PyCFunction)(void (*)(void))tree_fwd_bf16, METH_FASTCALL, NULL},
     {"keep_path", (PyCFunction)(void (*)(void))keep_path, METH_FASTCALL, NULL},
     {"int32_ptr", (PyCFunction)(void (*)(void))int32_ptr, METH_FASTCALL, NULL},
     {"bind", (PyCFunction)(void (*)(void))bind, METH_FASTCALL, NULL},

@@ -216,3 +216,56 @@ def test_reference_pool_restores_its_list():
     assert p.assign(lens, lens * 0, 0) is not None
     assert p.free == before and p.owned == owned
     assert p.assign(lens + 400, lens * 0, 0) is None and p.free == before
+
+
+def test_a_missing_scale_does_not_make_a_bf16_cache(L):
+    """The scale getters give NULL for a layer without static scales.  Passed
+    on, it must not be read as "bf16": twice the cache's bytes would be written
+    or read.  A bf16 cache has entry points of its own."""
+    assert call(L.fp8attn_kv_write, WRITE, qs=None) == INVALID
+    assert call(L.fp8attn_kv_tree_fwd, TREE, ds=None) == INVALID
+    write, tree = dict(WRITE), dict(TREE)
+    del write["qs"], tree["ds"]
+    f = L.fp8attn_kv_write_bf16
+    assert call(f, write, tokens=0) == OK
+    assert call(f, write, chead=136, tokens=0) == OK      # 16 bytes of bf16
+    for change, status in ((dict(tokens=-1), INVALID), (dict(k=None), INVALID),
+                           (dict(vc=None), INVALID), (dict(num=0), INVALID),
+                           (dict(dim=64), UNSUPPORTED), (dict(chead=132), UNSUPPORTED),
+                           (dict(kc=P(8)), UNSUPPORTED), (dict(tok=1001), UNSUPPORTED),
+                           (dict(tokens=1 << 28), UNSUPPORTED)):
+        assert call(f, write, **change) == status, change
+    f = L.fp8attn_kv_tree_fwd_bf16
+    assert call(f, tree, rows=0) == OK
+    assert call(f, tree, total=0, q=None, out=None) == OK
+    for change, status in ((dict(max_q=-1), INVALID), (dict(scale=-1.0), INVALID),
+                           (dict(words=0), INVALID), (dict(tables=None), INVALID),
+                           (dict(chead=120), UNSUPPORTED), (dict(mask=P(4)), UNSUPPORTED),
+                           (dict(ws=P(8)), UNSUPPORTED), (dict(rows=2049), UNSUPPORTED)):
+        assert call(f, tree, **change) == status, change
+
+
+def test_python_takes_no_null_scale(L):
+    import quantization_amax_reduce_b200 as qar
+    dev = torch.device("cpu")
+    with pytest.raises(ValueError, match="null"):
+        qar._scale3(0, "descale", True, dev)
+    with pytest.raises(ValueError, match="takes no"):
+        qar._scale3(0, "descale", False, dev)
+    assert qar._scale3(64, "descale", True, dev) == 64
+    C = qar._native()
+    plain = lambda d: [x.value or 0 if isinstance(x, P) else 0 if x is None else x  # noqa: E731
+                       for x in d.values()]
+    assert C.write(*plain(dict(WRITE, qs=None))) == INVALID
+    assert C.tree_fwd(*plain(dict(TREE, ds=None))) == INVALID
+    # the bf16 calls take the same arguments, with no scale
+    for f, good in ((C.write_bf16, dict(WRITE, qs=None, tokens=0)),
+                    (C.tree_fwd_bf16, dict(TREE, ds=None, rows=0))):
+        assert f(*plain(good)) == OK
+        assert f(*plain(dict(good, dim=64))) == UNSUPPORTED
+        assert f(*plain(dict(good, num=0))) == INVALID
+        with pytest.raises(TypeError, match="number of arguments"):
+            f(*plain(good)[:-1])
+    for f, good in ((C.write_bf16, WRITE), (C.tree_fwd_bf16, TREE)):
+        with pytest.raises(ValueError, match="no scale"):
+            f(*plain(good))
