@@ -482,7 +482,9 @@ cudaError_t launch_assign_pages(const AssignPagesLaunch& p, cudaStream_t stream)
   if (grid < 1) grid = 1;
   if (grid > 148) grid = 148;
   const size_t smem = 3 * (static_cast<size_t>(p.rows) + 1) * sizeof(int32_t);
-  if (smem > 48 * 1024) {
+  // a launch gets 48 KB unasked, for these sums and the kernel's own 400 bytes
+  // of shared variables (1024 are more than enough)
+  if (smem + 1024 > 48 * 1024) {
     // (always the largest size: calls of other threads with more rows rely on it)
     constexpr int kMost = 3 * (kMaxPageRows + 1) * static_cast<int>(sizeof(int32_t));
     static_assert(kMost <= 227 * 1024 - 1024, "shared memory of a CTA");

@@ -184,6 +184,30 @@ def test_assign_pages_of_two_threads_with_many_rows():
     assert not failed
 
 
+def test_assign_pages_just_below_the_shared_memory_of_a_plain_launch():
+    """Row counts whose prefix sums alone fit 48 KB of shared memory, but not
+    beside the kernel's own, in a process that made no larger call before."""
+    code = """if True:
+        import numpy as np, torch
+        from tests import kv_reference as ref
+        from tests.test_gpu_kv_cache import DevicePool, qar
+        for rows in (4061, 4062, 4080, 4095, 4096):
+            p = ref.Pool(rows, 2, 2 * rows, 16)
+            d = DevicePool(p)
+            seq, new = np.full(rows, 20), np.full(rows, 3)
+            want, got = p.assign(seq, new, 3 * rows), d.assign(seq, new, 3 * rows)
+            assert all(np.array_equal(g, w) for g, w in zip(got, want)), rows
+            assert qar.read_error_word(d.err) == 0
+            d.check(p)
+    """
+    import subprocess
+    import sys
+    from tests.conftest import ROOT
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True,
+                       timeout=600)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
 # ---------------------------------------------------------------------------
 # write
 # ---------------------------------------------------------------------------
