@@ -545,8 +545,10 @@ const float* fp8attn_static_descale_ptr(fp8attn_ctx* ctx, int layer);
  * empty step (cu all 0, slots -1): SEQLENS (new < 0, new > seq, seq beyond
  * table_width pages, owned outside [0, table_width], more than max_tokens new
  * tokens), PAGES (too few free pages, d_pool[0] out of range).  A page id
- * outside [0, num_pages) in a table or the free list sets PAGES too; its
- * tokens get slot -1.  Errors: INVALID (null or misaligned pointers, rows < 0,
+ * outside [0, num_pages) that this call meets in a table or the free list sets
+ * PAGES too: tokens in such a page get slot -1, a row that was to take it gets
+ * -1 instead, and one that is given back to the free list keeps its place there.
+ * Errors: INVALID (null or misaligned pointers, rows < 0,
  * num_pages < 1, table_width < 1, max_tokens < 0), UNSUPPORTED (page_size,
  * rows > 16384, num_pages >= 2^30, max_tokens >= 2^31), CUDA.  rows == 0
  * launches nothing, and needs max_tokens == 0. */

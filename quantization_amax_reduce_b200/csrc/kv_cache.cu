@@ -205,7 +205,12 @@ __global__ void __launch_bounds__(kPagesThreads) assign_pages_kernel(const Pages
       page[i] = dropped_of(static_cast<int>(min(k0 + i, static_cast<int64_t>(dropped) - 1)), row[i]);
 #pragma unroll
     for (int i = 0; i < kPagesPerThread; ++i)
-      if (k0 + i < dropped) a.free_pages[count + dropped - 1 - (k0 + i)] = page[i];
+      if (k0 + i < dropped) {
+        // (a bad id keeps its place, so that the list's length and order hold;
+        // whoever takes it is told again and does not follow it)
+        if (page[i] < 0 || page[i] >= a.num_pages) raise_error(a.err, kErrPages);
+        a.free_pages[count + dropped - 1 - (k0 + i)] = page[i];
+      }
   }
 
   // slots and positions, kTokensPerThread tokens at a time

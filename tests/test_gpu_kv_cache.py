@@ -121,6 +121,32 @@ def test_assign_pages_bad_page_ids_are_reported_and_not_followed():
     assert (slots[14:] == -1).all()                    # row 1: the bad new page
 
 
+@pytest.mark.parametrize("bad", [99, -1, -(2 ** 31)])
+def test_assign_pages_bad_page_ids_given_back_are_reported(bad):
+    """A page id outside the pool that a request gives back sets the error at
+    once, not in the step of the request that takes it next."""
+    p = ref.Pool(3, 4, 10, 16)
+    p.assign([20, 40, 5], [20, 40, 5], 65)
+    d = DevicePool(p)
+    d.tables[1, 1] = bad
+    d.assign([20, 10, 5], [0, 0, 0], 0)               # row 1 gives back its second and third
+    assert qar.read_error_word(d.err) == 7
+    p.tables[1, 1] = bad
+    p.assign([20, 10, 5], [0, 0, 0], 0)
+    d.check(p)                                        # (the list keeps its order and length)
+    # one that is passed on to a row that grows in the same step is not followed
+    q = ref.Pool(2, 4, 10, 16)
+    q.assign([40, 5], [40, 5], 45)
+    d = DevicePool(q)
+    d.tables[0, 1] = bad
+    _, slots, _ = d.assign([10, 40], [0, 35], 35)
+    assert qar.read_error_word(d.err) == 7
+    second = int(d.tables[0, 2])
+    assert d.tables[1].tolist()[:3] == [int(q.tables[1, 0]), -1, second]
+    assert (slots[:11] >= 0).all() and (slots[11:27] == -1).all()
+    assert (slots[27:] // 16 == second).all()
+
+
 def test_assign_pages_captured_at_a_fixed_size():
     """A step captured once, replayed over changing lengths."""
     r = np.random.Generator(np.random.PCG64(11))
