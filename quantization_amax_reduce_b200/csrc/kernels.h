@@ -171,6 +171,16 @@ struct KvTreeLaunch {
 
 constexpr int kMaxTreeRows = 2048;    // every CTA scans all rows
 
+// A CTA's range of work items is at least this many: below it another CTA and
+// the join of its piece cost more than the tiles they save.
+constexpr int kMinTreeItems = 4;
+
+// Items of a CTA's range, for up to 2^31 - 1 in all (no sum may pass that).
+__host__ __device__ constexpr int tree_items_per_cta(int total, int ctas) {
+  const int share = total > 0 ? (total - 1) / ctas + 1 : 0;
+  return share > kMinTreeItems ? share : kMinTreeItems;
+}
+
 // Work items (128-key tiles of a request's KV heads and query row tiles, and a
 // few more for each such unit) that lengths up to the given ones can come to.
 int64_t kv_tree_max_items(int rows, int max_q, int max_seqlen, int heads, int kv_heads);

@@ -312,7 +312,7 @@ kv_tree_keys_kernel(const __grid_constant__ CUtensorMap tm_k,
       const UnitRows<R>& col = ctl.rows[unit & 3];
       const Segment& seg = col.seg;   // (in shared memory: registers are short)
       if (threadIdx.x == 0 && seg.t0 == 0 && seg.t1 < seg.tiles)
-        a.join[blockIdx.x] = join_info(seg, items_per_cta(ctl.chunk[C::kThreads], gridDim.x));
+        a.join[blockIdx.x] = join_info(seg, tree_items_per_cta(ctl.chunk[C::kThreads], gridDim.x));
       const int ctx = seg.seq - seg.n;
       // columns in pairs: row sums of this thread's keys; kPOffset - ref, 0 while unset
       uint64_t sum2[kCols / 2], off2[kCols / 2];
@@ -777,7 +777,7 @@ kv_tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
       const UnitRows<R>& rows = ctl.rows[unit & 3];
       const Segment& seg = rows.seg;   // (in shared memory: registers are short)
       if (threadIdx.x == 0 && seg.t0 == 0 && seg.t1 < seg.tiles)
-        a.join[blockIdx.x] = join_info(seg, items_per_cta(ctl.chunk[C::kThreads], gridDim.x));
+        a.join[blockIdx.x] = join_info(seg, tree_items_per_cta(ctl.chunk[C::kThreads], gridDim.x));
       const int ctx = seg.seq - seg.n;
       // (not zero: a hidden score is -inf before it is multiplied)
       const float factor = rows.factor[row] == 0.0f ? 1.17549435e-38f : rows.factor[row];
@@ -1142,7 +1142,7 @@ int tile_rows(int max_q, int heads, int kv_heads) {
 
 int launch_ctas(int rows, int max_q, int max_seqlen, int heads, int kv_heads) {
   const int64_t items = kv_tree_max_items(rows, max_q, max_seqlen, heads, kv_heads);
-  const int64_t ctas = (items + kMinItems - 1) / kMinItems;
+  const int64_t ctas = (items + kMinTreeItems - 1) / kMinTreeItems;
   return static_cast<int>(ctas < 1 ? 1 : ctas < kMaxCtas ? ctas : kMaxCtas);
 }
 

@@ -10,6 +10,7 @@
 
 #include <cstdint>
 
+#include "kernels.h"
 #include "sm100_ptx.cuh"
 #include "state.cuh"
 
@@ -21,9 +22,6 @@ constexpr int kTile = 128;                 // keys of a tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kPOffset = 8.0f;           // log2 of P at the reference
 constexpr float kRefLag = 7.0f;
-// A CTA's range is at least this many items: below it another CTA and the
-// join of its piece cost more than the tiles they save.
-constexpr int kMinItems = 4;
 constexpr int kMaxCtas = 148;              // one per SM
 // What a unit costs beside its tiles (its Q, the way through the pipeline, its
 // epilogue), in tiles: ranges are cut by tiles plus this, or a CTA whose
@@ -275,11 +273,6 @@ struct Finder {
   }
 };
 
-// Items of a CTA's range.
-__device__ __forceinline__ int items_per_cta(int total, int ctas) {
-  return max(kMinItems, (total + ctas - 1) / ctas);
-}
-
 // The pieces of a unit that begins with `s`, which its CTA does not finish.
 __device__ __forceinline__ JoinInfo join_info(const Segment& s, int per) {
   return {s.q0, s.n, s.head, s.rt, 1 + (s.tiles - s.t1 + per - 1) / per};
@@ -292,7 +285,7 @@ struct Walker {
   int head = 0, rt = -1;     // the unit handed out last (its last tile was, too)
   __device__ __forceinline__ void init(const int* chunk, int ctas) {
     const int total = chunk[kThreads];
-    const int per = items_per_cta(total, ctas);
+    const int per = tree_items_per_cta(total, ctas);
     const int64_t from = static_cast<int64_t>(blockIdx.x) * per;
     w = static_cast<int>(min(from, static_cast<int64_t>(total)));
     end = static_cast<int>(min(from + per, static_cast<int64_t>(total)));

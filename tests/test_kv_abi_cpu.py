@@ -269,3 +269,23 @@ def test_python_takes_no_null_scale(L):
     for f, good in ((C.write_bf16, WRITE), (C.tree_fwd_bf16, TREE)):
         with pytest.raises(ValueError, match="no scale"):
             f(*plain(good))
+
+
+def test_shares_of_the_work_list_up_to_its_limit(tmp_path):
+    """The calls take bounds of up to 2^31 - 1 work items: a CTA's share of them
+    may not overflow on the way (the compiler refuses a constant that does)."""
+    import os
+    import subprocess
+    from quantization_amax_reduce_b200 import build
+    source = "#include \"kernels.h\"\nusing fp8attn::tree_items_per_cta;\n"
+    cases = [(0, 1, 4), (0, 148, 4), (1, 148, 4), (4, 1, 4), (592, 148, 4), (593, 148, 5),
+             (740, 148, 5), (741, 148, 6), (5, 1, 5)]
+    cases += [(t, n, -(-t // n)) for t in (2 ** 31 - 1, 2 ** 31 - 2, 2 ** 31 - 148, 2 ** 31 - 149)
+              for n in (1, 2, 147, 148)]
+    for total, ctas, want in cases:
+        source += f"static_assert(tree_items_per_cta({total}, {ctas}) == {want}, \"\");\n"
+    (tmp_path / "share.cpp").write_text(source)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(build.nvcc())), "include")
+    r = subprocess.run(["g++", "-std=c++17", "-fsyntax-only", "-w", "-I", build.CSRC, "-I", cuda,
+                        str(tmp_path / "share.cpp")], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[:2000]
