@@ -649,6 +649,14 @@ fp8attn_status fp8attn_kv_tree_fwd_bf16(const void* q, int64_t q_tok_stride, int
                                         float softmax_scale, void* out, void* workspace,
                                         size_t workspace_bytes, int32_t* d_error, void* stream);
 
+/* Self-test of the waits of the attention over the cache: in the calling
+ * thread's next fp8attn_kv_tree_fwd or fp8attn_kv_tree_fwd_bf16 that launches
+ * something, a CTA loads no K (which 0) or no V (which 1) from its tile-th
+ * 128-key tile on.  What waits for it gives up after the library's limit of
+ * 1 s, and the call reports TIMEOUT; later calls are not affected.  Host only.
+ * Errors: INVALID (which outside 0 and 1, tile < 0). */
+fp8attn_status fp8attn_selftest_kv_tree_stall(int which, int tile);
+
 /* After verification: request b keeps d_keep_lens[b] of its n_b drafted
  * nodes, d_paths[b][0] < d_paths[b][1] < ... (int32 [rows, depth], row stride
  * path_stride); their K and V rows move, in place, to nodes 0, 1, ... of the

@@ -126,6 +126,7 @@ def lib() -> ctypes.CDLL:
         "fp8attn_kv_tree_fwd_bf16": (I, [P, I64, I64, P, P, I64, I64, I64, I, I, P, I64, I, P, P,
                                          I, I, I, I64, I, I, I, P, I, F, P, P, ctypes.c_size_t, P,
                                          P]),
+        "fp8attn_selftest_kv_tree_stall": (I, [I, I]),
         "fp8attn_kv_keep_path": (I, [P, P, I64, I64, I64, I, I, I, I, I, P, I64, I, P, P, I, P,
                                      I64, I, P, P, P]),
         "fp8attn_apply_margin": (I, [P, I64, F, P]),
@@ -1013,6 +1014,14 @@ def selftest_bounded_waits(mbar_limit_ns: int = 50_000_000, device=None) -> int:
                                                 ctypes.c_void_p(_stream(None, dev))),
            "fp8attn_selftest_bounded_waits")
     return n.value
+
+
+def selftest_kv_tree_stall(which: str, tile: int) -> None:
+    """Stall this thread's next :func:`kv_tree_fwd`: its CTAs load no K (``"k"``)
+    or no V (``"v"``) from their ``tile``-th 128-key tile on, so that what waits
+    for it gives up after one second and the call reports a timeout."""
+    _check(lib().fp8attn_selftest_kv_tree_stall({"k": 0, "v": 1}[which], int(tile)),
+           "fp8attn_selftest_kv_tree_stall")
 
 
 def head_sharded_dynamic_quantize(ctx: "Context", layer: int, q: torch.Tensor, k: torch.Tensor,

@@ -902,6 +902,12 @@ fp8attn_status fp8attn_kv_tree_fwd_bf16(const void* q, int64_t q_tok_stride, int
                      mask_words, softmax_scale, out, workspace, workspace_bytes, d_error, stream);
 }
 
+fp8attn_status fp8attn_selftest_kv_tree_stall(int which, int tile) {
+  if (which < 0 || which > 1 || tile < 0) return FP8ATTN_ERR_INVALID;
+  stall_next_kv_tree(which == 1, tile);
+  return FP8ATTN_OK;
+}
+
 fp8attn_status fp8attn_kv_keep_path(void* k_cache, void* v_cache, int64_t page_stride,
                                     int64_t slot_stride, int64_t cache_head_stride, int num_pages,
                                     int page_size, int elem_bytes, int num_kv_heads, int head_dim,

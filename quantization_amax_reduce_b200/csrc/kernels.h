@@ -186,5 +186,8 @@ __host__ __device__ constexpr int tree_items_per_cta(int total, int ctas) {
 int64_t kv_tree_max_items(int rows, int max_q, int max_seqlen, int heads, int kv_heads);
 size_t kv_tree_workspace_bytes(int rows, int max_q, int max_seqlen, int heads, int kv_heads);
 cudaError_t launch_kv_tree(const KvTreeLaunch& p, cudaStream_t stream);
+// The calling thread's next launch_kv_tree loads no K (or V) from each CTA's
+// tile-th tile on, so that what waits for it gives up.
+void stall_next_kv_tree(bool v, int tile);
 
 }  // namespace fp8attn

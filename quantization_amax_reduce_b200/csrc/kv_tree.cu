@@ -1132,6 +1132,10 @@ bool make_cache_map(CUtensorMap* m, const void* base, const PagedCache& c) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Where this thread's next launch stalls its producers of K and V (self-test).
+constexpr int kNoStall = -1;
+thread_local int next_stall[2] = {kNoStall, kNoStall};
+
 // Query rows of a tile.  Up to 32 rows of a KV head: keys on the lanes, with
 // the fewest columns that hold them (16 is the smallest N); above: rows on the
 // lanes.
@@ -1211,6 +1215,8 @@ size_t kv_tree_workspace_bytes(int rows, int max_q, int max_seqlen, int heads, i
          ctas * sizeof(JoinInfo);
 }
 
+void stall_next_kv_tree(bool v, int tile) { next_stall[v] = tile; }
+
 cudaError_t launch_kv_tree(const KvTreeLaunch& p, cudaStream_t stream) {
   TreeArgs a;
   a.q = static_cast<const uint16_t*>(p.q);
@@ -1241,6 +1247,9 @@ cudaError_t launch_kv_tree(const KvTreeLaunch& p, cudaStream_t stream) {
   a.softmax_scale = p.softmax_scale;
   a.out = static_cast<__nv_bfloat16*>(p.out);
   a.err = p.err;
+  a.stall_k = next_stall[0];
+  a.stall_v = next_stall[1];
+  next_stall[0] = next_stall[1] = kNoStall;
   const int R = tile_rows(p.max_q, p.heads, p.cache.heads);
   const int ctas = launch_ctas(p.rows, p.max_q, p.max_seqlen, p.heads, p.cache.heads);
   a.part_o = static_cast<float*>(p.workspace);

@@ -53,6 +53,7 @@ struct TreeArgs {
   float2* part_ml;                       // [2 CTAs][R] {ref, sum}
   struct JoinInfo* join;                 // [CTAs] the unit that begins in a CTA and leaves it
   int32_t* err;
+  int stall_k, stall_v;                  // tile of a CTA at which its producer stops (self-test)
 };
 
 // A CTA's tiles [t0, t1) of one unit.
@@ -330,8 +331,10 @@ struct Walker {
 // once.  Warps that share a barrier must still agree on what comes next: the
 // preparing warps go through all of their units, but hand out no more of them,
 // and the softmax warps run on without data to the end of their unit, where
-// they vote on whether there is a next one.  Nothing is written out then.  (The whole warp tests: 64 cycles when the phase is over
-// already, against 117 for one lane and a warp sync.)
+// they vote on whether there is a next one.  Nothing is written out then.  The
+// flag may rise between two lanes' looks at it, so what a warp does as one goes
+// by its vote (any_aborted).  (The whole warp tests a barrier: 64 cycles when
+// the phase is over already, against 117 for one lane and a warp sync.)
 // ---------------------------------------------------------------------------
 
 struct Waits {
@@ -340,6 +343,10 @@ struct Waits {
   int lane;
   __device__ __forceinline__ bool aborted() const {
     return *const_cast<volatile int*>(abort_flag) != 0;
+  }
+  // the same for all lanes
+  __device__ __forceinline__ bool any_aborted() const {
+    return __any_sync(0xffffffffu, aborted());
   }
   __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity) const {
     if (!mbar_wait(bar, parity, const_cast<volatile int*>(abort_flag))) {
@@ -360,13 +367,14 @@ struct Waits {
 // stages): a box per page, one lane per page, page ids looked up a tile ahead.
 // A page id outside the cache is outside the tensor map: zeros arrive.  Before
 // stage i's n-th refill (n >= 1) it waits for phase n - 1 of free1[i], and of
-// free2[i] if there is one.  After an abort the copies go on, into stages that
-// nobody reads.
+// free2[i] if there is one.  After an abort there are no more copies: a stage
+// may then be given back whose last one never landed, and its barrier takes
+// another's bytes only in the next phase.
 // ---------------------------------------------------------------------------
 
 template <int R, int kThreads, bool kFp8>
 __device__ __forceinline__ void produce(const TreeArgs& a, const Waits& w, const int* chunk, const CUtensorMap* map,
-                        bool report, uint8_t* ring, int stages, uint64_t* full, uint64_t* free1,
+                        bool is_k, uint8_t* ring, int stages, uint64_t* full, uint64_t* free1,
                         uint64_t* free2) {
   constexpr int kBytes = kFp8 ? 16384 : 32768;   // of a tile
   const int page = 1 << a.page_log2;
@@ -376,7 +384,9 @@ __device__ __forceinline__ void produce(const TreeArgs& a, const Waits& w, const
   walk.init(chunk, gridDim.x);
   Segment seg;
   int g = 0, stage = 0, turn = 0;
-  while (!w.aborted() && walk.next(a, chunk, seg)) {
+  const int stall = is_k ? a.stall_k : a.stall_v;
+  bool stop = false;
+  while (!stop && walk.next(a, chunk, seg)) {
     const int32_t* table = a.tables + seg.b * a.table_stride;
     // this lane's first key of a tile; it has a page to load if the key is one
     auto first_key = [&](int t) { return t * kTile + (w.lane << box_log2); };
@@ -389,13 +399,15 @@ __device__ __forceinline__ void produce(const TreeArgs& a, const Waits& w, const
       const int id = next_id;
       if (t + 1 < seg.t1) next_id = look_up(t + 1);
       const bool load = has_page(t);   // (whatever its id: no id means "none")
-      if (report && load && (id < 0 || id >= a.num_pages)) raise_error(a.err, kErrPages);
+      if (is_k && load && (id < 0 || id >= a.num_pages)) raise_error(a.err, kErrPages);
       const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, load)) * box * (kFp8 ? 128 : 256);
       const int row = a.page_log2 > 7 ? (t * kTile) & (page - 1) : 0;
       if (turn > 0) {
         w.wait(&free1[stage], (turn - 1) & 1);
         if (free2) w.wait(&free2[stage], (turn - 1) & 1);
       }
+      stop = w.any_aborted() || g == stall;
+      if (stop) break;
       if (w.lane == 0) mbar_expect_tx(&full[stage], bytes);
       __syncwarp();
       if (load) {
@@ -691,7 +703,7 @@ __device__ __forceinline__ void prepare(const TreeArgs& a, const Waits& w, const
     seg = next;
     if (g > 0) s_done(g - 1);
     // (after an abort somebody may still use the unit that lies there)
-    const bool hand_out = !w.aborted();
+    const bool hand_out = !w.any_aborted();
     if (more)
       store_q<R, kFp8, kLoScale>(a, seg, q, sq, rows[unit & 3], row_max, barrier, unit_factor, tid,
                                  hand_out);

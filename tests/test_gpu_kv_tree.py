@@ -512,3 +512,31 @@ def test_any_page_id_outside_the_cache_reads_as_zeros(bad, nodes, fp8):
     assert qar.read_error_word(err) == 7
     s["values"] = [np.concatenate([v, np.zeros_like(v[:1])]) for v in s["values"]]
     check(out, *expect(s))
+
+
+@pytest.mark.parametrize("which,tile", [("k", 0), ("v", 0), ("k", 11), ("v", 14)])
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("nodes", [1, 4, 20])       # 16 and 32 columns, rows on the lanes
+def test_waits_that_give_up_end_the_call_with_a_timeout(nodes, fp8, which, tile):
+    """Loads that never come, at the start of a CTA's range or behind several of
+    its units: every wait ends, the call reports it, and the next one is right."""
+    seq = [1500, 200, 77, 900] * 12                 # some 26 tiles and their units a CTA
+    args = to_dev(make(43, seq, [nodes] * 48, 40, 8, 64, fp8))
+    want = qar.kv_tree_fwd(*args)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    qar.selftest_kv_tree_stall(which, tile)
+    qar.kv_tree_fwd(*args, error=err)
+    torch.cuda.synchronize()
+    assert qar.read_error_word(err) == 3
+    for _ in range(3):
+        assert torch.equal(qar.kv_tree_fwd(*args, error=err), want)
+    assert qar.read_error_word(err) == 0
+
+
+def test_a_stall_behind_the_last_tile_changes_nothing():
+    args = to_dev(make(44, [700, 30], [3, 1], 8, 2, 16, True))
+    want = qar.kv_tree_fwd(*args)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    qar.selftest_kv_tree_stall("k", 10 ** 6)
+    assert torch.equal(qar.kv_tree_fwd(*args, error=err), want)
+    assert qar.read_error_word(err) == 0

@@ -289,3 +289,8 @@ def test_shares_of_the_work_list_up_to_its_limit(tmp_path):
     r = subprocess.run(["g++", "-std=c++17", "-fsyntax-only", "-w", "-I", build.CSRC, "-I", cuda,
                         str(tmp_path / "share.cpp")], capture_output=True, text=True)
     assert r.returncode == 0, r.stderr[:2000]
+
+
+def test_stall_self_test_checks_its_arguments(L):
+    for which, tile in ((-1, 0), (2, 0), (0, -1)):
+        assert L.fp8attn_selftest_kv_tree_stall(which, tile) == INVALID
