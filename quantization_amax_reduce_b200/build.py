@@ -1,6 +1,7 @@
 """Build ``libfp8attn.so`` in-tree with nvcc for sm_100a (B200), and beside it
 the small CPython module ``_calls`` (gcc) through which the binding makes the
-calls that take only microseconds.
+calls that take only microseconds.  The library needs nvcc alone; the module
+needs Python's headers, and is left out with a warning where there are none.
 
     python -m quantization_amax_reduce_b200.build [--force] [--verbose]
 
@@ -14,6 +15,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -47,6 +49,11 @@ def _stale() -> bool:
 def _build_calls(force: bool) -> None:
     if not force and not _older(CALLS, [CALLS_SRC, os.path.join(ROOT, "include", "fp8attn.h")]):
         return
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        # (nothing but the paged cache's Python functions needs it)
+        warnings.warn("no Python.h: _calls is not built; without it kv_assign_pages, kv_write, "
+                      "kv_tree_fwd and kv_keep_path raise an error in Python")
+        return
     cc = os.environ.get("CC") or shutil.which("gcc") or shutil.which("cc")
     if not cc:
         raise RuntimeError("no C compiler found")
@@ -58,9 +65,14 @@ def _build_calls(force: bool) -> None:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    """The library first: it needs neither Python's headers nor the module."""
+    if force or _stale():
+        _build_lib(verbose)
     _build_calls(force)
-    if not force and not _stale():
-        return LIB
+    return LIB
+
+
+def _build_lib(verbose: bool) -> None:
     objdir = os.path.join(ROOT, "_build")
     os.makedirs(objdir, exist_ok=True)
     objs = []
@@ -76,7 +88,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     tmp = LIB + ".tmp"
     subprocess.check_call([nvcc()] + ARCH + ["-shared", "-o", tmp] + objs)
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":

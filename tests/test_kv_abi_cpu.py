@@ -294,3 +294,38 @@ def test_shares_of_the_work_list_up_to_its_limit(tmp_path):
 def test_stall_self_test_checks_its_arguments(L):
     for which, tile in ((-1, 0), (2, 0), (0, -1)):
         assert L.fp8attn_selftest_kv_tree_stall(which, tile) == INVALID
+
+
+def test_build_without_pythons_headers(tmp_path, monkeypatch):
+    """The library is built where Python's headers are missing, as before there
+    was a CPython module beside it; what needs the module says so."""
+    import os
+    import subprocess
+    import quantization_amax_reduce_b200 as qar
+    from quantization_amax_reduce_b200 import build
+    monkeypatch.setattr(build, "LIB", str(tmp_path / "libfp8attn.so"))
+    monkeypatch.setattr(build, "CALLS", str(tmp_path / "_calls.so"))
+    monkeypatch.setattr(build.sysconfig, "get_paths", lambda *a, **k: {"include": str(tmp_path)})
+
+    def compiler(cmd, **kw):
+        if build.CALLS_SRC in cmd and not os.path.exists(tmp_path / "Python.h"):
+            raise subprocess.CalledProcessError(1, cmd)
+        target = cmd[cmd.index("-o") + 1]
+        if target.startswith(str(tmp_path)):
+            open(target, "w").close()
+
+    monkeypatch.setattr(build.subprocess, "check_call", compiler)
+    with pytest.warns(UserWarning, match="Python.h"):
+        assert build.build() == build.LIB
+    assert os.path.exists(build.LIB) and not os.path.exists(build.CALLS)
+    (tmp_path / "Python.h").write_text("")
+    build.build()
+    assert os.path.exists(build.CALLS)
+
+    def no_module(*a):
+        raise ImportError("no _calls")
+
+    monkeypatch.setattr(qar, "_native_calls", None)
+    monkeypatch.setattr(qar.importlib, "import_module", no_module)
+    with pytest.raises(RuntimeError, match="_calls module is missing"):
+        qar._native()
