@@ -84,6 +84,7 @@ using namespace kv_tree;
 // one with deep rings reads 6.4 (16 columns, E4M3).
 template <int R, bool kFp8>
 struct KeysCfg {
+  static_assert(R == 16 || R == 32, "columns of a tile");
   static constexpr int kGroups = 2;
   static constexpr int kCols = R / kGroups;               // columns of a softmax thread
   static constexpr int kSoftmaxWarps = 4 * kGroups, kSoftmaxThreads = 128 * kGroups;
@@ -291,7 +292,7 @@ kv_tree_keys_kernel(const __grid_constant__ CUtensorMap tm_k,
         [&](int g) { w.wait(&ctl.s_full[g % C::kKStages], (g / C::kKStages) & 1); }, wait_pv);
   } else {
     // ------------------------------------------------------------ softmax
-    constexpr int kCols = C::kCols, kPart = kCols < 16 ? kCols : 16;
+    constexpr int kCols = C::kCols;
     const int wg = warp >> 2, wq = warp & 3;
     const int key = 32 * wq + lane;                 // lane of TMEM: key, or channel
     const int bar_wg = 1 + wg;
@@ -300,7 +301,7 @@ kv_tree_keys_kernel(const __grid_constant__ CUtensorMap tm_k,
     const uint32_t t_o = tmem + lane_off + C::kO + wg * kCols;
     const int col0 = wg * kCols;
     const int c_mine = lane & (kCols - 1);          // where a lane stands for a column
-    constexpr uint32_t kAll = kCols == 32 ? 0xffffffffu : (1u << kCols) - 1;
+    constexpr uint32_t kAll = (1u << kCols) - 1;
     // this key's row of P; 16-byte pieces are swizzled by address bits 7 and up
     uint8_t* prow = sp + key * C::kPitch;
     const int pswz = R == 32 ? (key >> 1) & 3 : (key >> 2) & 1;
@@ -355,18 +356,14 @@ kv_tree_keys_kernel(const __grid_constant__ CUtensorMap tm_k,
         uint64_t x2[kCols / 2];
         {
           const uint64_t sixteenth = f2_pack(0.0625f, 0.0625f);
+          uint32_t u[kCols], v[kCols];
+          tmem_ld<kCols>(t_s + (g & 1) * C::kN, u);
+          if (kFp8) tmem_ld<kCols>(t_s + (g & 1) * C::kN + R, v);
+          tmem_ld_wait();
 #pragma unroll
-          for (int h = 0; h < kCols; h += kPart) {
-            uint32_t u[kPart], v[kPart];
-            tmem_ld<kPart>(t_s + (g & 1) * C::kN + h, u);
-            if (kFp8) tmem_ld<kPart>(t_s + (g & 1) * C::kN + R + h, v);
-            tmem_ld_wait();
-#pragma unroll
-            for (int c = 0; c < kPart; c += 2) {
-              x2[(h + c) / 2] = f2_bits(u[c], u[c + 1]);
-              if (kFp8)
-                x2[(h + c) / 2] = f2_fma(f2_bits(v[c], v[c + 1]), sixteenth, x2[(h + c) / 2]);
-            }
+          for (int c = 0; c < kCols; c += 2) {
+            x2[c / 2] = f2_bits(u[c], u[c + 1]);
+            if (kFp8) x2[c / 2] = f2_fma(f2_bits(v[c], v[c + 1]), sixteenth, x2[c / 2]);
           }
           if (!kFp8 || one_factor) {
             const uint64_t f2 = f2_pack(factor, factor);

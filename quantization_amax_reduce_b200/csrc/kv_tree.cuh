@@ -105,15 +105,13 @@ __device__ __forceinline__ bool group_any(int id, int threads, bool yes) {
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
   if constexpr (N == 8) tmem_ld8(taddr, r);
-  else if constexpr (N == 16) tmem_ld16(taddr, r);
-  else tmem_ld32(taddr, r);
+  else tmem_ld16(taddr, r);
 }
 
 template <int N>
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[N]) {
   if constexpr (N == 8) tmem_st8(taddr, r);
-  else if constexpr (N == 16) tmem_st16(taddr, r);
-  else tmem_st32(taddr, r);
+  else tmem_st16(taddr, r);
 }
 
 // A pair times a power of two (exact but for what leaves the type's range).
@@ -126,7 +124,7 @@ __device__ __forceinline__ uint32_t scale_bf16x2(uint32_t x, float s) {
   return cvt_bf16x2(__uint_as_float(x << 16) * s, __uint_as_float(x & 0xFFFF0000u) * s);
 }
 
-// Reduces N columns (a power of two up to 32) over the warp's lanes: lane l
+// Reduces N columns (8 or 16) over the warp's lanes: lane l
 // gets column l % N.  N - 1 + log2(32 / N) shuffles instead of 5 N.
 template <int N, bool kMax>
 __device__ __forceinline__ float reduce_columns(float (&v)[N], int lane) {

@@ -258,7 +258,7 @@ __host__ __device__ constexpr uint32_t make_idesc(uint32_t a_fmt, uint32_t b_fmt
 constexpr uint32_t kIdescAMnMajor = 1u << 15;
 
 // Swizzling modes of a shared-memory matrix descriptor.
-constexpr uint64_t kSwizzle128 = 2, kSwizzle64 = 4, kSwizzle32 = 6;
+constexpr uint64_t kSwizzle64 = 4, kSwizzle32 = 6;
 
 // Shared-memory matrix descriptor of a swizzling mode (lbo and sbo as below).
 __device__ __forceinline__ uint64_t make_sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo,
