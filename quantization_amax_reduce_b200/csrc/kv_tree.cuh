@@ -386,17 +386,19 @@ __device__ __forceinline__ void produce(const TreeArgs& a, const Waits& w, const
   bool stop = false;
   while (!stop && walk.next(a, chunk, seg)) {
     const int32_t* table = a.tables + seg.b * a.table_stride;
-    // this lane's first key of a tile; it has a page to load if the key is one
+    // this lane's first key of a tile; it has a page to load if that lies before
+    // `last`
+    const int last = w.lane < kTile >> box_log2 ? seg.seq : 0;
     auto first_key = [&](int t) { return t * kTile + (w.lane << box_log2); };
-    auto has_page = [&](int t) { return w.lane < kTile >> box_log2 && first_key(t) < seg.seq; };
     auto look_up = [&](int t) {
-      return has_page(t) ? __ldg(table + (first_key(t) >> a.page_log2)) : 0;
+      if (first_key(t) >= last) return 0;
+      return __ldg(table + (first_key(t) >> a.page_log2));
     };
     int next_id = look_up(seg.t0);
     for (int t = seg.t0; t < seg.t1; ++t, ++g) {
       const int id = next_id;
       if (t + 1 < seg.t1) next_id = look_up(t + 1);
-      const bool load = has_page(t);   // (whatever its id: no id means "none")
+      const bool load = first_key(t) < last;   // (whatever its id: no id means "none")
       if (is_k && load && (id < 0 || id >= a.num_pages)) raise_error(a.err, kErrPages);
       const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, load)) * box * (kFp8 ? 128 : 256);
       const int row = a.page_log2 > 7 ? (t * kTile) & (page - 1) : 0;
@@ -424,7 +426,6 @@ __device__ __forceinline__ void produce(const TreeArgs& a, const Waits& w, const
   __syncwarp();
 }
 
-// ---------------------------------------------------------------------------
 // 128-row tiles with at most 64 rows hold them twice: rows 64 to 127 are rows 0
 // to 63 again, and take the second half of a tile's keys.
 template <int R>
@@ -432,6 +433,7 @@ __device__ __forceinline__ bool is_doubled(const TreeArgs& a, const Segment& s) 
   return R == 128 && s.n * a.group - s.rt * R <= 64;
 }
 
+// ---------------------------------------------------------------------------
 // Q of a unit: a half warp per row, 8 channels a lane, four rows of a half warp
 // at a time, the first four loaded a unit ahead.  K-major rows of 128 bytes,
 // 128-byte swizzle; bf16: two 64-channel halves; E4M3: hi tile, then the
