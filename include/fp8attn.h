@@ -500,9 +500,10 @@ int fp8attn_quantize_qkv_noalloc_error(void* stream);
 /* ------------------------------------------------------------------ */
 /* Paged KV cache                                                      */
 /*                                                                     */
-/* K and V kept from step to step ("Quantized KV Cache", vLLM-Omni     */
-/* docs: the KV cache quantised to FP8 with per-tensor scales, listed  */
-/* layers in the native dtype; the pages say nothing of its layout).   */
+/* K and V kept from step to step, for the language half of a model    */
+/* whose layers have static scales or keep the native dtype.  (The     */
+/* pages' own "KV cache" is one forward pass's K and V; a stored cache */
+/* is this library's addition.)                                        */
 /* A cache holds num_pages pages of page_size slots (a power of two,   */
 /* 8 to 1024); element (slot s, head h, channel d) of K or V is at     */
 /*   base + (s / page_size) * page_stride + (s % page_size) *          */
@@ -536,9 +537,12 @@ const float* fp8attn_static_descale_ptr(fp8attn_ctx* ctx, int layer);
  * {free pages, 0}; the second word is the kernel's and is 0 between calls.
  *   d_cu_new: int32[rows + 1], first new token of each row;
  *   d_slots: int64[max_tokens], d_positions: int32[max_tokens] (16-byte
- *     aligned): slot and position of each new token; behind the last, up to
- *     max_tokens, slots are -1 and positions 0 (a step captured at a fixed
- *     size: fp8attn_kv_write skips them).
+ *     aligned): slot and place in the sequence of each new token; behind the
+ *     last, up to max_tokens, slots are -1 and positions 0 (a step captured at a
+ *     fixed size: fp8attn_kv_write skips them).  A drafted tree's nodes lie one
+ *     behind the other, so a node's place is the context's length plus its
+ *     index; its rotary position is that length plus its depth, which the caller
+ *     knows from the tree (fp8attn_kv_keep_path moves K as it was rotated).
  * Block table entries that no new page takes stay as they are.  Rows must not
  * share pages that this call gives back; calls on one pool must not overlap.
  * Device-side errors change nothing of the tables and the pool and give an

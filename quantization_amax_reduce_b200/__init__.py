@@ -689,8 +689,10 @@ def kv_assign_pages(seq_lens: torch.Tensor, new_lens: torch.Tensor, block_tables
     their last ones back (length 0: a request that ended).  ``block_tables``
     [rows, width], ``owned`` [rows], ``free_pages`` [num_pages] and ``pool``
     ({free pages, 0}) are int32 and updated in place.  Returns (cu_new int32
-    [rows + 1], slots int64 [max_tokens], positions int32 [max_tokens]); slots
-    behind the last new token are -1, which :func:`kv_write` skips.  Too few
+    [rows + 1], slots int64 [max_tokens], positions int32 [max_tokens]: a
+    token's place in its sequence, which for a node of a drafted tree is not its
+    rotary position, context + depth); slots behind the last new token are -1,
+    which :func:`kv_write` skips.  Too few
     free pages or inconsistent lengths change nothing and set ``error`` (see
     fp8attn_kv_assign_pages in fp8attn.h)."""
     _require_cuda(seq_lens, "seq_lens")

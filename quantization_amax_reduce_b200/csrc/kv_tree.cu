@@ -27,8 +27,8 @@
 //   warps 11-14 the next unit's Q into shared memory; V: E4M3 -> f16 into the
 //               buffer that the product reads, and the rows that must not touch
 //               it (past the sequence, non-finite)
-// One lane of a warp waits and arrives for it: 256 threads that each try the
-// same mbarrier cost some 250 cycles a time.
+// A warp waits on a barrier as a whole, and one lane arrives for it: 256
+// threads that each arrive cost some 250 cycles a time.
 //
 // E4M3 cache: K feeds kind::f8f6f4 as it lies.  A row of Q (bf16), scaled by a
 // power of two (its tile's, where the rows are within 2^4 of each other) to
@@ -38,7 +38,12 @@
 // nothing of Q is lost.  V is
 // widened to f16 (exact) on its way and P is f16, 2^8 at the reference: P in
 // E4M3 would cost 2.6 % rms per key, and its 2^-18 range would drop the
-// far tail of a long context.  bf16 cache: bf16 products, P bf16.
+// far tail of a long context.  A P below 2^-25, 2^-33 of the reference, becomes
+// 0.  Error against 64 bits 1.7e-3 of the result, which is what rounding the
+// output to bf16 costs by itself.  bf16 cache: bf16 products, and P in bf16,
+// since a product's two operands have one type and bf16 V does not fit f16's
+// range: 2.2e-3.  Row sums are fp32 sums of P before its rounding: a key's
+// weight is off by that rounding, 2^-11 of it (f16) or 2^-8 (bf16) at most.
 //
 // Reference: ref starts at the first tile's maximum and moves only when a
 // score exceeds it by more than 7 (2^15 stays inside f16): then P never
@@ -54,7 +59,7 @@
 // and a second kernel joins them in order: results do not depend on timing.
 //
 // Bound: HBM for long contexts.  8 requests x 32768 tokens, 8 KV heads: E4M3
-// with 8 query rows a head 91 us (5.9 TB/s, 0.90 of a copy's rate), with 32 111
+// with 8 query rows a head 91 us (5.9 TB/s, 0.90 of a copy's rate), with 32 112
 // us; bf16 with 8 rows 169 us (6.4 TB/s, 0.97).  For short contexts the latency
 // of a unit's stages, some 6000 cycles: 128 chains of 4 over 5 to 300 tokens, 16
 // heads, 60 us where the bytes take 25.  A call starts and joins in about 10 us.
@@ -840,7 +845,10 @@ kv_tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
         // ---- P, in one pass: 32 scores become 16 words over scores that were
         // read already.  A row whose 32 scores exceed its reference by more than
         // kRefLag moves it by a whole power of two, which rescales the row's
-        // earlier P of this tile, its sum and O without rounding.
+        // earlier P of this tile, its sum and O without rounding.  (But for P in
+        // f16 that falls below 2^-14: it loses bits, below 2^-25 all of them.
+        // Against the new maximum, which is above 2^7, that is at most 2^-32 a
+        // key, far less than P's rounding at the maximum.)
         const uint64_t f2 = f2_pack(factor, factor);
 #pragma unroll 1
         for (int h = h0; h < h1; ++h) {
